@@ -459,6 +459,101 @@ MOE_API int moe_block_forward(const moe_bf16* x, int64_t N, const moe_block_dims
                               const moe_act_cfg* act, moe_bf16* out, int32_t* topk_idx_out,
                               float* topk_w_out, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------- 8-bit block-scaled forms (FP8)
+ *
+ * The pages run their experts in bf16; the models they show are also served in
+ * 8 bits.  These entry points take and give one format: e4m3 values q with
+ * fp32 scales, value = q * scale, where
+ *   rows of activations [M, K] carry one scale per 128 columns,
+ *     scale [M, ceil(K/128)];
+ *   weights [B, N, K] carry one scale per 128 x 128 block,
+ *     scale [B, ceil(N/128), ceil(K/128)].
+ * Blocks at the ends may be partial.  Limits: K (the contracted width) a
+ * multiple of 16, N (an output width) a multiple of 8; e4m3 and bf16 pointers
+ * 16-byte aligned, scales 4-byte aligned.  Scales are the caller's: any fp32
+ * values, not only those that moe_quantize_fp8 gives.  Products are summed in
+ * fp32: 128 columns of K in the tensor core, times the two scales, then over
+ * the blocks; one rounding to bf16 at the end. */
+typedef uint8_t moe_fp8; /* e4m3 bit pattern (no infinities, NaN 0x7f) */
+
+/* bf16 to the 8-bit format.  x [B, M, K] bf16; q [B, M, K] e4m3.
+ * block_rows 1 (activations): scale [B, M, ceil(K/128)];
+ * block_rows 128 (weights): scale [B, ceil(M/128), ceil(K/128)].  Per block:
+ *   a = max |x|, s = fl32(max(a, 2^-100) / 448); with pow2_scales != 0, s is
+ *   rounded up to a power of two;  q = e4m3(fl32(x * fl32(1/s))), to nearest
+ *   even, at most 448 in magnitude;  scale = s.
+ * A NaN or an infinity in a block makes its scale NaN or infinite (and a
+ * product with its row NaN).  No workspace, no device-side failure. */
+MOE_API int moe_quantize_fp8(const moe_bf16* x, int64_t B, int64_t M, int K, int block_rows,
+                             int pow2_scales, moe_fp8* q, float* scale, void* stream);
+
+/* moe_dispatch with the rows quantised as they are gathered: sorted row j of
+ * (xq, x_scale) is row perm[j] / K of x_e as moe_quantize_fp8 (block_rows 1)
+ * gives it.  counts, offsets, perm, pos, workspace and errors as moe_dispatch;
+ * d_e a multiple of 16; xq [S, d_e] e4m3 and x_scale [S, ceil(d_e/128)] fp32
+ * are not optional. */
+MOE_API int moe_dispatch_fp8(const int32_t* topk_idx, int64_t N, int K, int E,
+                             const moe_bf16* x_e, int d_e, int pow2_scales, int32_t* counts,
+                             int32_t* offsets, int32_t* perm, int32_t* pos, moe_fp8* xq,
+                             float* x_scale, void* ws, size_t ws_bytes, void* stream);
+
+/* moe_linear on 8-bit operands: y[m, n] = bf16( sum_k x[m, k] * W[n, k]
+ * (+ residual[m, n]) ), rounded once.  xq [M, K], w [N_out, K]; residual
+ * (may be NULL) and y [M, N_out] bf16.  y may be the residual buffer. */
+MOE_API size_t moe_linear_fp8_workspace_size(int64_t M, int K, int N_out);
+MOE_API int moe_linear_fp8(const moe_fp8* xq, const float* x_scale, int64_t M, int K,
+                           const moe_fp8* w, const float* w_scale, int N_out,
+                           const moe_bf16* residual, moe_bf16* y, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* One product per expert over ragged row segments: for rows j of segment e
+ * (offsets[e] <= j < offsets[e+1]), y[j, :] = bf16( x[j, :] . w[e]^T ).
+ * xq [S, K]; offsets [E+1] int32 on the device, offsets[0] = 0, non-decreasing,
+ * offsets[E] <= S; w [E, N_out, K]; y [S, N_out] bf16.  Empty segments cost
+ * nothing; rows from offsets[E] on are neither read nor written.  A segment
+ * that runs backwards or past S is left out and recorded as
+ * MOE_ERR_DEVICE_BOUNDS. */
+MOE_API size_t moe_grouped_linear_fp8_workspace_size(int64_t S, int K, int E, int N_out);
+MOE_API int moe_grouped_linear_fp8(const moe_fp8* xq, const float* x_scale,
+                                   const int32_t* offsets, int E, int64_t S, int K,
+                                   const moe_fp8* w, const float* w_scale, int N_out, moe_bf16* y,
+                                   void* ws, size_t ws_bytes, void* stream);
+
+/* The experts' weights in the 8-bit format: w1, w3 [E, F, d_e], w2 [E, d_e, F]
+ * and their block scales. */
+typedef struct moe_fp8_experts {
+  const moe_fp8* w1;
+  const moe_fp8* w3;
+  const moe_fp8* w2;
+  const float* w1_scale; /* [E, ceil(F/128), ceil(d_e/128)] */
+  const float* w3_scale; /* [E, ceil(F/128), ceil(d_e/128)] */
+  const float* w2_scale; /* [E, ceil(d_e/128), ceil(F/128)] */
+} moe_fp8_experts;
+
+/* moe_expert_ffn on 8-bit operands: g = x . w1[e]^T and u = x . w3[e]^T in
+ * fp32, h = act(g, u) in fp32 (moe_act_cfg's functions without their bf16
+ * roundings), h to the 8-bit format per row and 128 columns as
+ * moe_quantize_fp8 does (power-of-two scales with pow2_scales != 0),
+ * y = bf16( h . w2[e]^T ).  offsets as in moe_grouped_linear_fp8; d_e and F
+ * multiples of 16. */
+MOE_API size_t moe_expert_ffn_fp8_workspace_size(int64_t S, int d_e, int E, int F);
+MOE_API int moe_expert_ffn_fp8(const moe_fp8* xq, const float* x_scale, const int32_t* offsets,
+                               int E, int64_t S, int d_e, int F, const moe_fp8_experts* w,
+                               const moe_act_cfg* act, int pow2_scales, moe_bf16* y, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/* moe_forward with 8-bit experts: moe_route -> moe_dispatch_fp8 ->
+ * moe_expert_ffn_fp8 -> moe_combine, on one stream with no host
+ * synchronisation.  Arguments as moe_forward; pow2_scales is the form of the
+ * scales given to the tokens and to h. */
+MOE_API size_t moe_forward_fp8_workspace_size(int64_t N, int d_r, int d_e,
+                                              const moe_route_cfg* cfg, int F);
+MOE_API int moe_forward_fp8(const moe_bf16* x_r, const moe_bf16* x_e, int64_t N, int d_r, int d_e,
+                            const float* W, const float* bias, const moe_route_cfg* cfg,
+                            const moe_fp8_experts* experts, int F, const moe_act_cfg* act,
+                            int pow2_scales, moe_bf16* out, int32_t* topk_idx_out,
+                            float* topk_w_out, void* ws, size_t ws_bytes, void* stream);
+
 /* --------------------------------------------------------------- status */
 
 /* Reads (synchronising `stream`) and clears the device status word of a
@@ -480,8 +575,8 @@ MOE_API uint64_t moe_launch_count(void);
  * time limit, records MOE_ERR_DEVICE_TIMEOUT in the status word and stops the
  * kernel cleanly (its other roles stop, its tensor memory is freed), so a
  * broken protocol cannot hang the GPU.  With on != 0 the grouped expert GEMM
- * kernels launched afterwards (moe_expert_ffn, moe_forward and every entry
- * point built on them) make that path run: before issuing any copy, each
+ * kernels launched afterwards (moe_expert_ffn, moe_forward, their 8-bit forms
+ * and every entry point built on them) make that path run: before issuing any copy, each
  * CTA's producer waits on a barrier that nothing arrives on, with a 1 ms
  * limit; the wait runs out, the call's status word reads
  * MOE_ERR_DEVICE_TIMEOUT and its outputs are left unwritten.  on = 0 (the

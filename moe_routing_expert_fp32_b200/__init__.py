@@ -11,6 +11,7 @@ binding's functions raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -130,6 +131,11 @@ class BlockWeights:
                                for n, _ in _BlockWeights._fields_])
 
 
+class _Fp8Experts(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w1", "w3", "w2", "w1_scale", "w3_scale",
+                                               "w2_scale")]
+
+
 @dataclass(frozen=True)
 class ActConfig:
     kind: str = "silu"        # "silu" or "situ"
@@ -151,7 +157,11 @@ EXPORTS = ("moe_route_workspace_size", "moe_route", "moe_route_from_logits",
            "moe_block_forward", "moe_shared_experts_workspace_size", "moe_shared_experts",
            "moe_ep_expert_ffn_workspace_size", "moe_ep_expert_ffn", "moe_expert_ffn_gathered",
            "moe_ep_dispatch_rows", "moe_ep_combine_rows", "moe_launch_count",
-           "moe_set_wait_probe", "moe_expert_ffn_to_slots")
+           "moe_set_wait_probe", "moe_expert_ffn_to_slots", "moe_quantize_fp8", "moe_dispatch_fp8",
+           "moe_linear_fp8_workspace_size", "moe_linear_fp8",
+           "moe_grouped_linear_fp8_workspace_size", "moe_grouped_linear_fp8",
+           "moe_expert_ffn_fp8_workspace_size", "moe_expert_ffn_fp8",
+           "moe_forward_fp8_workspace_size", "moe_forward_fp8")
 
 
 def lib() -> ctypes.CDLL:
@@ -167,6 +177,7 @@ def lib() -> ctypes.CDLL:
     rc, ac, ev = ctypes.POINTER(_RouteCfg), ctypes.POINTER(_ActCfg), ctypes.POINTER(_StageEvents)
     bd, bw = ctypes.POINTER(_BlockDims), ctypes.POINTER(_BlockWeights)
     pr = ctypes.POINTER(_PeerRows)
+    xw = ctypes.POINTER(_Fp8Experts)
     sig = {
         "moe_route_workspace_size": ([i64, i32, rc], sz),
         "moe_route": ([vp, i64, i32, vp, vp, rc, vp, vp, vp, sz, vp], i32),
@@ -203,6 +214,19 @@ def lib() -> ctypes.CDLL:
         "moe_set_wait_probe": ([i32], i32),
         "moe_expert_ffn_to_slots": ([vp, vp, vp, i32, i64, i32, i32, vp, vp, vp, ac, vp, vp, sz,
                                      vp], i32),
+        "moe_quantize_fp8": ([vp, i64, i64, i32, i32, i32, vp, vp, vp], i32),
+        "moe_dispatch_fp8": ([vp, i64, i32, i32, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz,
+                              vp], i32),
+        "moe_linear_fp8_workspace_size": ([i64, i32, i32], sz),
+        "moe_linear_fp8": ([vp, vp, i64, i32, vp, vp, i32, vp, vp, vp, sz, vp], i32),
+        "moe_grouped_linear_fp8_workspace_size": ([i64, i32, i32, i32], sz),
+        "moe_grouped_linear_fp8": ([vp, vp, vp, i32, i64, i32, vp, vp, i32, vp, vp, sz, vp], i32),
+        "moe_expert_ffn_fp8_workspace_size": ([i64, i32, i32, i32], sz),
+        "moe_expert_ffn_fp8": ([vp, vp, vp, i32, i64, i32, i32, xw, ac, i32, vp, vp, sz, vp],
+                               i32),
+        "moe_forward_fp8_workspace_size": ([i64, i32, i32, rc, i32], sz),
+        "moe_forward_fp8": ([vp, vp, i64, i32, i32, vp, vp, rc, xw, i32, ac, i32, vp, vp, vp, vp,
+                             sz, vp], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -626,4 +650,236 @@ def block_forward(x, weights: BlockWeights, cfg: RouteConfig, act: ActConfig, no
            lib().moe_block_forward(_ptr(x), N, ctypes.byref(dims), ctypes.byref(wc),
                                    ctypes.byref(c), ctypes.byref(a), _ptr(out), _ptr(topk_idx),
                                    _ptr(topk_w), _ptr(ws), ws.numel(), _stream()))
+    return out
+
+
+# ------------------------------------------------- 8-bit block-scaled forms
+def _fp8_args(*named):
+    """Checks (name, tensor, dtype, shape) entries: contiguous CUDA tensors of one
+    device, of that dtype and shape (None: any).  Returns the device."""
+    dev = named[0][1].device
+    for name, t, dtype, shape in named:
+        if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, {named[0][0]} on {dev}")
+    return dev
+
+
+def _on(dev):
+    """Makes `dev` current for the calls inside, when it is not already."""
+    torch = _torch()
+    if torch.cuda.current_device() == dev.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _ws_for(ws, need, dev):
+    torch = _torch()
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    if ws.device != dev:
+        raise ValueError(f"ws is on {ws.device}, expected {dev}")
+    return ws
+
+
+def _c128(n):
+    return (n + 127) // 128
+
+
+def quantize_fp8(x, block_rows: int = 1, pow2_scales: bool = False, q=None, scale=None):
+    """bf16 to e4m3 with fp32 block scales (moe_quantize_fp8): returns (q, scale).
+
+    block_rows 1 (activations): x [..., K], one scale per row and 128 columns,
+    scale [..., ceil(K/128)].  block_rows 128 (weights): x [N, K] or
+    [E, N, K], one scale per 128 x 128 block, scale [..., ceil(N/128),
+    ceil(K/128)].  pow2_scales rounds the scales up to powers of two."""
+    torch = _torch()
+    shape = x.shape
+    if block_rows == 1:
+        if len(shape) < 1:
+            raise ValueError("x needs at least one dimension")
+        B, K = 1, shape[-1]
+        M = x.numel() // K if K else 0
+        s_shape = (*shape[:-1], _c128(K))
+    else:
+        if len(shape) not in (2, 3):
+            raise ValueError("x must be [N, K] or [E, N, K] with block_rows = 128")
+        M, K = shape[-2], shape[-1]
+        B = shape[0] if len(shape) == 3 else 1
+        s_shape = (*shape[:-2], _c128(M), _c128(K))
+    named = [("x", x, torch.bfloat16, None)]
+    if q is not None:
+        named.append(("q", q, torch.float8_e4m3fn, shape))
+    if scale is not None:
+        named.append(("scale", scale, torch.float32, s_shape))
+    dev = _fp8_args(*named)
+    q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev) if q is None else q
+    scale = torch.empty(s_shape, dtype=torch.float32, device=dev) if scale is None else scale
+    with _on(dev):
+        _check("moe_quantize_fp8",
+               lib().moe_quantize_fp8(_ptr(x), B, M, K, block_rows, int(pow2_scales), _ptr(q),
+                                      _ptr(scale), _stream()))
+    return q, scale
+
+
+def dispatch_fp8(topk_idx, x_e, num_experts: int, pow2_scales: bool = False, ws=None):
+    """dispatch() with the rows quantised as they are gathered
+    (moe_dispatch_fp8): (counts [E], offsets [E+1], perm [S], pos [S],
+    xq [S, d_e] e4m3, x_scale [S, ceil(d_e/128)])."""
+    torch = _torch()
+    N, K = topk_idx.shape
+    d_e = x_e.shape[1]
+    E, S = num_experts, N * K
+    dev = _fp8_args(("x_e", x_e, torch.bfloat16, (N, d_e)),
+                    ("topk_idx", topk_idx, torch.int32, None))
+    i32 = torch.int32
+    counts = torch.empty(E, dtype=i32, device=dev)
+    offsets = torch.empty(E + 1, dtype=i32, device=dev)
+    perm = torch.empty(S, dtype=i32, device=dev)
+    pos = torch.empty(S, dtype=i32, device=dev)
+    xq = torch.empty((S, d_e), dtype=torch.float8_e4m3fn, device=dev)
+    xs = torch.empty((S, _c128(d_e)), dtype=torch.float32, device=dev)
+    ws = _ws_for(ws, lib().moe_dispatch_workspace_size(N, K, E), dev)
+    with _on(dev):
+        _check("moe_dispatch_fp8",
+               lib().moe_dispatch_fp8(_ptr(topk_idx), N, K, E, _ptr(x_e), d_e, int(pow2_scales),
+                                      _ptr(counts), _ptr(offsets), _ptr(perm), _ptr(pos),
+                                      _ptr(xq), _ptr(xs), _ptr(ws), ws.numel(), _stream()))
+    return counts, offsets, perm, pos, xq, xs
+
+
+def linear_fp8(xq, x_scale, w, w_scale, residual=None, out=None, ws=None):
+    """bf16(x . W^T (+ residual)) of 8-bit operands (moe_linear_fp8): xq [M, K],
+    x_scale [M, ceil(K/128)], w [N_out, K], w_scale [ceil(N_out/128),
+    ceil(K/128)]."""
+    torch = _torch()
+    M, K = xq.shape
+    N = w.shape[0]
+    f8, f32, bf = torch.float8_e4m3fn, torch.float32, torch.bfloat16
+    named = [("xq", xq, f8, None), ("x_scale", x_scale, f32, (M, _c128(K))),
+             ("w", w, f8, (N, K)), ("w_scale", w_scale, f32, (_c128(N), _c128(K)))]
+    if residual is not None:
+        named.append(("residual", residual, bf, (M, N)))
+    if out is not None:
+        named.append(("out", out, bf, (M, N)))
+    dev = _fp8_args(*named)
+    need = lib().moe_linear_fp8_workspace_size(M, K, N)
+    if need == 0:
+        raise MoeError("moe_linear_fp8_workspace_size", -2)
+    ws = _ws_for(ws, need, dev)
+    out = torch.empty((M, N), dtype=bf, device=dev) if out is None else out
+    with _on(dev):
+        _check("moe_linear_fp8",
+               lib().moe_linear_fp8(_ptr(xq), _ptr(x_scale), M, K, _ptr(w), _ptr(w_scale), N,
+                                    _ptr(residual), _ptr(out), _ptr(ws), ws.numel(), _stream()))
+    return out
+
+
+def grouped_linear_fp8(xq, x_scale, offsets, w, w_scale, out=None, ws=None):
+    """One 8-bit product per expert over the row segments offsets[e] ..
+    offsets[e+1]-1 (moe_grouped_linear_fp8): xq [S, K], w [E, N_out, K],
+    w_scale [E, ceil(N_out/128), ceil(K/128)]; returns [S, N_out] bf16, whose
+    rows from offsets[E] on are left as they were."""
+    torch = _torch()
+    S, K = xq.shape
+    E, N, _ = w.shape
+    f8, f32, bf = torch.float8_e4m3fn, torch.float32, torch.bfloat16
+    named = [("xq", xq, f8, None), ("x_scale", x_scale, f32, (S, _c128(K))),
+             ("offsets", offsets, torch.int32, (E + 1,)), ("w", w, f8, (E, N, K)),
+             ("w_scale", w_scale, f32, (E, _c128(N), _c128(K)))]
+    if out is not None:
+        named.append(("out", out, bf, (S, N)))
+    dev = _fp8_args(*named)
+    need = lib().moe_grouped_linear_fp8_workspace_size(S, K, E, N)
+    if need == 0:
+        raise MoeError("moe_grouped_linear_fp8_workspace_size", -2)
+    ws = _ws_for(ws, need, dev)
+    out = torch.empty((S, N), dtype=bf, device=dev) if out is None else out
+    with _on(dev):
+        _check("moe_grouped_linear_fp8",
+               lib().moe_grouped_linear_fp8(_ptr(xq), _ptr(x_scale), _ptr(offsets), E, S, K,
+                                            _ptr(w), _ptr(w_scale), N, _ptr(out), _ptr(ws),
+                                            ws.numel(), _stream()))
+    return out
+
+
+def _fp8_experts(w1, w1_scale, w3, w3_scale, w2, w2_scale):
+    """The (name, tensor, dtype, shape) checks and the C struct of the 8-bit experts."""
+    torch = _torch()
+    E, F, d = w1.shape
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    up = (E, _c128(F), _c128(d))
+    named = [("w1", w1, f8, None), ("w1_scale", w1_scale, f32, up), ("w3", w3, f8, (E, F, d)),
+             ("w3_scale", w3_scale, f32, up), ("w2", w2, f8, (E, d, F)),
+             ("w2_scale", w2_scale, f32, (E, _c128(d), _c128(F)))]
+    return named, _Fp8Experts(*[t.data_ptr() for t in (w1, w3, w2, w1_scale, w3_scale, w2_scale)])
+
+
+def expert_ffn_fp8(xq, x_scale, offsets, w1, w1_scale, w3, w3_scale, w2, w2_scale, act: ActConfig,
+                   pow2_scales: bool = False, y=None, ws=None):
+    """The expert MLP on 8-bit rows and weights (moe_expert_ffn_fp8): xq [S, d]
+    sorted by expert, w1, w3 [E, F, d], w2 [E, d, F] with their block scales;
+    returns [S, d] bf16, whose rows from offsets[E] on are left as they were."""
+    torch = _torch()
+    S, d = xq.shape
+    E, F, _ = w1.shape
+    named, xw = _fp8_experts(w1, w1_scale, w3, w3_scale, w2, w2_scale)
+    named += [("xq", xq, torch.float8_e4m3fn, (S, w1.shape[2])),
+              ("x_scale", x_scale, torch.float32, (S, _c128(d))),
+              ("offsets", offsets, torch.int32, (E + 1,))]
+    if y is not None:
+        named.append(("y", y, torch.bfloat16, (S, d)))
+    dev = _fp8_args(*named)
+    need = lib().moe_expert_ffn_fp8_workspace_size(S, d, E, F)
+    if need == 0:
+        raise MoeError("moe_expert_ffn_fp8_workspace_size", -2)
+    ws = _ws_for(ws, need, dev)
+    y = torch.empty((S, d), dtype=torch.bfloat16, device=dev) if y is None else y
+    a = act._c()
+    with _on(dev):
+        _check("moe_expert_ffn_fp8",
+               lib().moe_expert_ffn_fp8(_ptr(xq), _ptr(x_scale), _ptr(offsets), E, S, d, F,
+                                        ctypes.byref(xw), ctypes.byref(a), int(pow2_scales),
+                                        _ptr(y), _ptr(ws), ws.numel(), _stream()))
+    return y
+
+
+def forward_fp8(x_r, W, bias, cfg: RouteConfig, w1, w1_scale, w3, w3_scale, w2, w2_scale,
+                act: ActConfig, x_e=None, pow2_scales: bool = False, ws=None, out=None,
+                topk_idx=None, topk_w=None):
+    """The routed MoE layer with 8-bit experts (moe_forward_fp8): route,
+    dispatch_fp8, expert_ffn_fp8 and combine.  Arguments as forward(), with the
+    experts' weights in the 8-bit format.  Returns ``out`` [N, d_e] bf16."""
+    torch = _torch()
+    N, d_r = x_r.shape
+    E, F, d_e = w1.shape
+    if E != cfg.num_experts:
+        raise ValueError("w1 does not hold num_experts experts")
+    if x_e is None and d_e != d_r:
+        raise ValueError("x_e is required when the experts' width differs from the router's")
+    named, xw = _fp8_experts(w1, w1_scale, w3, w3_scale, w2, w2_scale)
+    named += [("x_r", x_r, torch.bfloat16, None), ("W", W, torch.float32, (E, d_r))]
+    for name, t, dtype, shape in (("x_e", x_e, torch.bfloat16, (N, d_e)),
+                                  ("bias", bias, torch.float32, (E,)),
+                                  ("out", out, torch.bfloat16, (N, d_e)),
+                                  ("topk_idx", topk_idx, torch.int32, (N, cfg.top_k)),
+                                  ("topk_w", topk_w, torch.float32, (N, cfg.top_k))):
+        if t is not None:
+            named.append((name, t, dtype, shape))
+    dev = _fp8_args(*named)
+    c, a = cfg._c(), act._c()
+    need = lib().moe_forward_fp8_workspace_size(N, d_r, d_e, ctypes.byref(c), F)
+    if need == 0:
+        raise MoeError("moe_forward_fp8_workspace_size", -2)
+    ws = _ws_for(ws, need, dev)
+    out = torch.empty((N, d_e), dtype=torch.bfloat16, device=dev) if out is None else out
+    with _on(dev):
+        _check("moe_forward_fp8",
+               lib().moe_forward_fp8(_ptr(x_r), _ptr(x_e), N, d_r, d_e, _ptr(W), _ptr(bias),
+                                     ctypes.byref(c), ctypes.byref(xw), F, ctypes.byref(a),
+                                     int(pow2_scales), _ptr(out), _ptr(topk_idx), _ptr(topk_w),
+                                     _ptr(ws), ws.numel(), _stream()))
     return out

@@ -1,6 +1,7 @@
 // api.cu -- the C ABI of libmoe: argument validation, workspace layout, launch
 // sequencing.  Nothing here computes the layer; every step runs in the
-// kernels of router.cu, dispatch.cu, expert_gemm.cu and combine.cu.
+// kernels of router.cu, dispatch.cu, expert_gemm.cu, combine.cu, quantize_fp8.cu
+// and gemm_fp8.cu.
 #include <math.h>
 
 #include <nvtx3/nvToolsExt.h>
@@ -607,6 +608,283 @@ int moe_forward(const moe_bf16* x_r, const moe_bf16* x_e, int64_t N, int d_r, in
   }
   if (events && !rec(events->after_combine)) return MOE_ERR_CUDA;
   return MOE_OK;
+}
+
+// -------------------------------------------------- 8-bit block-scaled forms
+namespace {
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+int64_t ceil128(int64_t v) { return (v + 127) / 128; }
+
+int check_fp8_product(int64_t S, int K, int E, int N) {
+  if (S < 0 || K <= 0 || E < 1 || N <= 0) return MOE_ERR_INVALID_ARG;
+  if (E > 1024 || K % 16 != 0 || N % 8 != 0 || S > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int check_fp8_ffn_shape(int64_t S, int d_e, int E, int F) {
+  const int rc = check_fp8_product(S, d_e, E, 8);
+  if (rc) return rc;
+  return check_fp8_product(S, F, E, d_e);  // the down product contracts over F
+}
+
+// pointers of a grouped product's operands
+int check_fp8_operands(int64_t S, const moe_fp8* xq, const float* x_scale, const moe_fp8* w,
+                       const float* w_scale, const moe_bf16* residual, const moe_bf16* y) {
+  if (!w || !w_scale) return MOE_ERR_INVALID_ARG;
+  if (S > 0 && (!xq || !x_scale || !y)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w) || !aligned4(w_scale)) return MOE_ERR_ALIGNMENT;
+  if (S > 0 && (!aligned16(xq) || !aligned4(x_scale) || !aligned16(y) ||
+                (residual && !aligned16(residual))))
+    return MOE_ERR_ALIGNMENT;
+  return MOE_OK;
+}
+}  // namespace
+
+int moe_quantize_fp8(const moe_bf16* x, int64_t B, int64_t M, int K, int block_rows,
+                     int pow2_scales, moe_fp8* q, float* scale, void* stream) {
+  if (B < 0 || M < 0 || K <= 0 || (block_rows != 1 && block_rows != 128))
+    return MOE_ERR_INVALID_ARG;
+  if (K % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (B > INT32_MAX || M > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const int64_t row_blocks = B * (block_rows == 1 ? M : ceil128(M));  // < 2^62
+  if (row_blocks > INT32_MAX * (int64_t)(block_rows == 1 ? 16 : 1) / ceil128(K))
+    return MOE_ERR_UNSUPPORTED;
+  const bool some = B > 0 && M > 0;
+  if (some && (!x || !q || !scale)) return MOE_ERR_INVALID_ARG;
+  if (some && (!aligned16(x) || !aligned16(q) || !aligned4(scale))) return MOE_ERR_ALIGNMENT;
+  int rc;
+  if ((rc = check_device())) return rc;
+  if (!some) return MOE_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(x);
+  const cudaError_t e =
+      block_rows == 1
+          ? launch_quantize_rows(xb, B * M, K, pow2_scales != 0, q, scale, nullptr, 0, 0, s)
+          : launch_quantize_blocks(xb, B, M, K, pow2_scales != 0, q, scale, s);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int moe_dispatch_fp8(const int32_t* topk_idx, int64_t N, int K, int E, const moe_bf16* x_e,
+                     int d_e, int pow2_scales, int32_t* counts, int32_t* offsets, int32_t* perm,
+                     int32_t* pos, moe_fp8* xq, float* x_scale, void* ws, size_t ws_bytes,
+                     void* stream) {
+  if (N < 0 || K < 1 || E < 1 || d_e <= 0) return MOE_ERR_INVALID_ARG;
+  if (E > 1024 || K > 16) return MOE_ERR_UNSUPPORTED;
+  if (d_e % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (N > INT32_MAX / K) return MOE_ERR_UNSUPPORTED;
+  if (!counts || !offsets) return MOE_ERR_INVALID_ARG;
+  if (N > 0 && (!topk_idx || !perm || !pos || !x_e || !xq || !x_scale)) return MOE_ERR_INVALID_ARG;
+  if (N > 0 && (!aligned16(x_e) || !aligned16(xq) || !aligned4(x_scale))) return MOE_ERR_ALIGNMENT;
+  int rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_dispatch_workspace_size(N, K, E)))) return rc;
+  if ((rc = check_device())) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((rc = reset_status(ws, s))) return rc;
+  if (N == 0) {
+    if (cudaMemsetAsync(counts, 0, sizeof(int32_t) * E, s) != cudaSuccess ||
+        cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (E + 1), s) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(x_e);
+  if (launch_dispatch(topk_idx, N, K, E, x, d_e, counts, offsets, perm, pos, nullptr,
+                      reinterpret_cast<int32_t*>(body_of(ws)), status_of(ws), s) != cudaSuccess ||
+      launch_quantize_rows(x, N, d_e, pow2_scales != 0, xq, x_scale, pos, K, N * K, s) !=
+          cudaSuccess)
+    return MOE_ERR_CUDA;
+  return MOE_OK;
+}
+
+size_t moe_grouped_linear_fp8_workspace_size(int64_t S, int K, int E, int N_out) {
+  if (check_fp8_product(S, K, E, N_out) != MOE_OK) return 0;
+  return kStatusBytes;
+}
+
+int moe_grouped_linear_fp8(const moe_fp8* xq, const float* x_scale, const int32_t* offsets, int E,
+                           int64_t S, int K, const moe_fp8* w, const float* w_scale, int N_out,
+                           moe_bf16* y, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_fp8_product(S, K, E, N_out);
+  if (rc) return rc;
+  if (!offsets) return MOE_ERR_INVALID_ARG;
+  if ((rc = check_fp8_operands(S, xq, x_scale, w, w_scale, nullptr, y))) return rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_grouped_linear_fp8_workspace_size(S, K, E, N_out))))
+    return rc;
+  if ((rc = check_device())) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((rc = reset_status(ws, s))) return rc;
+  if (S == 0) return MOE_OK;
+  return grouped_fp8_run(xq, x_scale, offsets, E, S, K, w, w_scale, N_out, nullptr,
+                         reinterpret_cast<__nv_bfloat16*>(y), status_of(ws), s, false);
+}
+
+size_t moe_linear_fp8_workspace_size(int64_t M, int K, int N_out) {
+  if (check_fp8_product(M, K, 1, N_out) != MOE_OK) return 0;
+  return kStatusBytes;
+}
+
+int moe_linear_fp8(const moe_fp8* xq, const float* x_scale, int64_t M, int K, const moe_fp8* w,
+                   const float* w_scale, int N_out, const moe_bf16* residual, moe_bf16* y,
+                   void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_fp8_product(M, K, 1, N_out);
+  if (rc) return rc;
+  if ((rc = check_fp8_operands(M, xq, x_scale, w, w_scale, residual, y))) return rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_linear_fp8_workspace_size(M, K, N_out)))) return rc;
+  if ((rc = check_device())) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((rc = reset_status(ws, s))) return rc;
+  if (M == 0) return MOE_OK;
+  return grouped_fp8_run(xq, x_scale, nullptr, 1, M, K, w, w_scale, N_out,
+                         reinterpret_cast<const __nv_bfloat16*>(residual),
+                         reinterpret_cast<__nv_bfloat16*>(y), status_of(ws), s, false);
+}
+
+namespace {
+int check_fp8_experts(const moe_fp8_experts* w) {
+  if (!w || !w->w1 || !w->w3 || !w->w2 || !w->w1_scale || !w->w3_scale || !w->w2_scale)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w->w1) || !aligned16(w->w3) || !aligned16(w->w2) || !aligned4(w->w1_scale) ||
+      !aligned4(w->w3_scale) || !aligned4(w->w2_scale))
+    return MOE_ERR_ALIGNMENT;
+  return MOE_OK;
+}
+}  // namespace
+
+size_t moe_expert_ffn_fp8_workspace_size(int64_t S, int d_e, int E, int F) {
+  if (check_fp8_ffn_shape(S, d_e, E, F) != MOE_OK) return 0;
+  return kStatusBytes + expert_fp8_scratch_bytes(S, F);
+}
+
+int moe_expert_ffn_fp8(const moe_fp8* xq, const float* x_scale, const int32_t* offsets, int E,
+                       int64_t S, int d_e, int F, const moe_fp8_experts* w,
+                       const moe_act_cfg* act, int pow2_scales, moe_bf16* y, void* ws,
+                       size_t ws_bytes, void* stream) {
+  int rc = check_fp8_ffn_shape(S, d_e, E, F);
+  if (rc) return rc;
+  if ((rc = check_act(act))) return rc;
+  if (!offsets) return MOE_ERR_INVALID_ARG;
+  if ((rc = check_fp8_experts(w))) return rc;
+  if (S > 0 && (!xq || !x_scale || !y)) return MOE_ERR_INVALID_ARG;
+  if (S > 0 && (!aligned16(xq) || !aligned4(x_scale) || !aligned16(y))) return MOE_ERR_ALIGNMENT;
+  if ((rc = check_ws(ws, ws_bytes, moe_expert_ffn_fp8_workspace_size(S, d_e, E, F)))) return rc;
+  if ((rc = check_device())) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((rc = reset_status(ws, s))) return rc;
+  if (S == 0) return MOE_OK;
+  return expert_ffn_fp8_run(xq, x_scale, offsets, E, S, d_e, F, w->w1, w->w1_scale, w->w3,
+                            w->w3_scale, w->w2, w->w2_scale, *act, pow2_scales != 0,
+                            reinterpret_cast<__nv_bfloat16*>(y), body_of(ws), status_of(ws), s);
+}
+
+namespace {
+struct ForwardFp8Layout {
+  size_t stage, idx, w, counts, offsets, perm, pos, xq, xs, y, total;
+};
+
+ForwardFp8Layout forward_fp8_layout(int64_t N, int d_r, int d_e, int E, int K, int F) {
+  ForwardFp8Layout L{};
+  const int64_t S = N * K;
+  size_t stage = route_body(N, d_r, E);
+  const size_t disp = dispatch_scratch_bytes(S, E);
+  const size_t exp = expert_fp8_scratch_bytes(S, F);
+  if (disp > stage) stage = disp;
+  if (exp > stage) stage = exp;
+  size_t o = kStatusBytes;
+  auto take = [&](size_t* at, size_t bytes) {
+    *at = o;
+    o += align_up(bytes, 256);
+  };
+  take(&L.stage, stage);
+  take(&L.idx, sizeof(int32_t) * (size_t)S);
+  take(&L.w, sizeof(float) * (size_t)S);
+  take(&L.counts, sizeof(int32_t) * (size_t)E);
+  take(&L.offsets, sizeof(int32_t) * (size_t)(E + 1));
+  take(&L.perm, sizeof(int32_t) * (size_t)S);
+  take(&L.pos, sizeof(int32_t) * (size_t)S);
+  take(&L.xq, (size_t)S * (size_t)d_e);
+  take(&L.xs, sizeof(float) * (size_t)S * (size_t)ceil128(d_e));
+  take(&L.y, sizeof(__nv_bfloat16) * (size_t)S * (size_t)d_e);
+  L.total = o;
+  return L;
+}
+
+int check_forward_fp8(int64_t N, int d_r, int d_e, const moe_route_cfg* cfg, int F) {
+  int rc = check_route_cfg(cfg);
+  if (rc) return rc;
+  if (N < 0 || d_r <= 0) return MOE_ERR_INVALID_ARG;
+  if (N > INT32_MAX / cfg->top_k || d_r % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  return check_fp8_ffn_shape(N * cfg->top_k, d_e, cfg->num_experts, F);
+}
+}  // namespace
+
+size_t moe_forward_fp8_workspace_size(int64_t N, int d_r, int d_e, const moe_route_cfg* cfg,
+                                      int F) {
+  if (check_forward_fp8(N, d_r, d_e, cfg, F) != MOE_OK) return 0;
+  return forward_fp8_layout(N, d_r, d_e, cfg->num_experts, cfg->top_k, F).total;
+}
+
+int moe_forward_fp8(const moe_bf16* x_r, const moe_bf16* x_e, int64_t N, int d_r, int d_e,
+                    const float* W, const float* bias, const moe_route_cfg* cfg,
+                    const moe_fp8_experts* experts, int F, const moe_act_cfg* act,
+                    int pow2_scales, moe_bf16* out, int32_t* topk_idx_out, float* topk_w_out,
+                    void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_forward_fp8(N, d_r, d_e, cfg, F);
+  if (rc) return rc;
+  if ((rc = check_act(act))) return rc;
+  if (!x_e) {
+    if (d_e != d_r) return MOE_ERR_INVALID_ARG;
+    x_e = x_r;
+  }
+  if (!W) return MOE_ERR_INVALID_ARG;
+  if ((rc = check_fp8_experts(experts))) return rc;
+  if (N > 0 && (!x_r || !out)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(W)) return MOE_ERR_ALIGNMENT;
+  if (N > 0 && (!aligned16(x_r) || !aligned16(x_e) || !aligned16(out))) return MOE_ERR_ALIGNMENT;
+  const int E = cfg->num_experts, K = cfg->top_k;
+  const ForwardFp8Layout L = forward_fp8_layout(N, d_r, d_e, E, K, F);
+  if ((rc = check_ws(ws, ws_bytes, L.total))) return rc;
+  if ((rc = check_device())) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((rc = reset_status(ws, s))) return rc;
+  if (N == 0) return MOE_OK;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  DeviceStatus* st = status_of(ws);
+  uint8_t* stage = base + L.stage;
+  int32_t* idx = topk_idx_out ? topk_idx_out : reinterpret_cast<int32_t*>(base + L.idx);
+  float* w = topk_w_out ? topk_w_out : reinterpret_cast<float*>(base + L.w);
+  int32_t* offsets = reinterpret_cast<int32_t*>(base + L.offsets);
+  int32_t* pos = reinterpret_cast<int32_t*>(base + L.pos);
+  uint8_t* xq = base + L.xq;
+  float* xs = reinterpret_cast<float*>(base + L.xs);
+  __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(base + L.y);
+  const Range layer("moe.forward_fp8");
+  {
+    const Range r("moe.route");
+    if ((rc = route_impl(reinterpret_cast<const __nv_bfloat16*>(x_r), N, d_r, W, bias, *cfg, idx,
+                         w, stage, st, s)))
+      return rc;
+  }
+  {
+    const Range r("moe.dispatch_fp8");
+    const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(x_e);
+    if (launch_dispatch(idx, N, K, E, x, d_e, reinterpret_cast<int32_t*>(base + L.counts),
+                        offsets, reinterpret_cast<int32_t*>(base + L.perm), pos, nullptr,
+                        reinterpret_cast<int32_t*>(stage), st, s) != cudaSuccess ||
+        launch_quantize_rows(x, N, d_e, pow2_scales != 0, xq, xs, pos, K, N * K, s) !=
+            cudaSuccess)
+      return MOE_ERR_CUDA;
+  }
+  {
+    const Range r("moe.expert_ffn_fp8");
+    if ((rc = expert_ffn_fp8_run(xq, xs, offsets, E, N * K, d_e, F, experts->w1,
+                                 experts->w1_scale, experts->w3, experts->w3_scale, experts->w2,
+                                 experts->w2_scale, *act, pow2_scales != 0, y, stage, st, s)))
+      return rc;
+  }
+  const Range r("moe.combine");
+  return launch_combine(y, pos, w, N, K, d_e, N * K, reinterpret_cast<__nv_bfloat16*>(out), st,
+                        s) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
 }
 
 // ------------------------------------------------------------ dense layers

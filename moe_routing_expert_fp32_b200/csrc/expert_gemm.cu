@@ -54,6 +54,11 @@
 #include "sm100.cuh"
 
 namespace moe {
+
+// The diagnostics hook's switch (moe_set_wait_probe), read at every launch.
+static std::atomic<int> g_wait_probe{0};
+int wait_probe() { return g_wait_probe.load(std::memory_order_relaxed); }
+
 namespace {
 
 constexpr int BM = 128;        // A rows per tile (MMA M)
@@ -151,7 +156,6 @@ __device__ __forceinline__ uint32_t idesc_bf16(int n) {
 // issues any copy; the wait runs out and the kernel takes its abort path (the
 // error recorded, the other roles stopped, TMEM freed).  Returns true when the
 // kernel must stop.
-constexpr uint64_t kProbeLimitNs = 1000000ull;
 __device__ __forceinline__ bool probe_abort(int probe, uint64_t* never, volatile int* abort_flag,
                                             DeviceStatus* st, int detail) {
   if (!probe) return false;
@@ -1324,10 +1328,6 @@ bool make_map_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-// The diagnostics hook's switch (moe_set_wait_probe), read at every launch.
-std::atomic<int> g_wait_probe{0};
-int wait_probe() { return g_wait_probe.load(std::memory_order_relaxed); }
 
 template <int MODE, int NTMAX, int STAGES, int UM, int KSUB>
 cudaError_t launch_gemm(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b,

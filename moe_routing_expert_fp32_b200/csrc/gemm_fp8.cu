@@ -1,0 +1,651 @@
+// gemm_fp8.cu -- products of 8-bit block-scaled operands on the 5th-generation
+// tensor cores: the dense Linear, the Linear grouped by expert over ragged row
+// segments, and the expert MLP (gate/up products, activation, requantisation;
+// down product).
+//
+//   y[m, n] = sum_b  sx[m, b] * sw[n / 128, b] * sum_{k in block b} qx[m, k] qw[n, k]
+//
+// The scales change every 128 columns of K, so a product cannot run through K
+// in the tensor core's accumulator: the MMAs of one K block (4 of K = 32,
+// kind::f8f6f4, e4m3 x e4m3 -> fp32) write a fresh TMEM buffer, and the epilogue
+// warps add it, times sx * sw, to fp32 sums in registers, while the MMAs of the
+// next block fill another buffer.
+//
+// Layout: token rows are the MMA's M side (TMEM lane = token row), weight rows
+// its N side.  Each thread then owns part of one row: its scale of a K block is
+// one register times one value shared by the warp, and the largest |h| of a
+// 128-column block is a maximum over its own registers (and one neighbour's).
+//   * gate_up: the N side is 128 rows of w1 over the same 128 rows of w3, so a
+//     unit yields whole 128-column blocks of h, which it rounds to e4m3 itself;
+//   * M is 128 rows whatever the segment: a decode tile (TM = 32) loads only its
+//     rows and lets the MMA read on into the weights behind them, which fills
+//     accumulator lanes that nothing reads.
+// Roles: 8 epilogue warps (lane quarter = warp % 4, column half = warp / 4), one
+// TMA warp, one MMA warp; a ring of stages guarded by mbarriers; a persistent
+// grid over units (token tile, weight block), weight block fastest.  Every wait
+// is bounded as in expert_gemm.cu.
+#include <cuda.h>
+
+#include "fp8.cuh"
+#include "moe_internal.cuh"
+#include "sm100.cuh"
+
+namespace moe {
+namespace {
+
+using sm100::mbar_arrive;
+using sm100::mbar_arrive_expect_tx;
+using sm100::mbar_init;
+using sm100::mbar_wait;
+using sm100::smem_u32;
+using sm100::tc_fence_after;
+using sm100::tc_fence_before;
+using sm100::tma_load_2d;
+using sm100::tma_load_3d;
+using sm100::umma_commit;
+
+constexpr int BM = 128;        // MMA M: token rows
+constexpr int BK = 128;        // K per stage = scale block = one 128-byte swizzle row
+constexpr int UK = 32;         // K per tcgen05.mma for 8-bit inputs
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp, MMA warp
+constexpr int kTmemCols = 512;
+constexpr int kSmallBox = 16;  // token rows per small TMA box
+constexpr int kMaxSegments = 1024;
+
+constexpr int kBarBytes = 320;
+// On the abort path: how long a role waits for copies or MMAs still in flight.
+constexpr uint64_t kDrainNs = 100000000ull;
+
+enum Mode { kPlain = 0, kGateUp = 1 };
+
+template <int MODE, int BN, int TM, int STAGES>
+struct Cfg {
+  static constexpr int kABytes = TM * BK;
+  static constexpr int kBBytes = BN * BK;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kBufs = kTmemCols / BN;
+  static constexpr int kQuarters = TM / 32;  // lane quarters that can hold rows
+  static constexpr int kStartBytes = (kMaxSegments + 1) * 4;
+  static constexpr int kAmaxBytes = 2 * 2 * BM * 4;  // unit parity x half x row
+  static constexpr size_t kSmem = (size_t)STAGES * kStageBytes + 1024 + kBarBytes +
+                                  kAmaxBytes + kStartBytes;
+  static_assert(kABytes % 1024 == 0 && kBBytes % 1024 == 0, "1024-byte aligned operands");
+  static_assert(kStageBytes >= BM * BK, "the MMA's 128 A rows stay inside the ring");
+  static_assert(MODE == kPlain || BN == 256, "gate_up: 128 rows of w1 and of w3");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+struct Args {
+  const int32_t* offsets;  // [E + 1], or nullptr: one segment of all S rows
+  int E;
+  int64_t S;
+  int N;    // output columns (gate_up: d_ff)
+  int K;
+  const float* xs;   // [S, KB]
+  const float* ws0;  // [E, NB, KB]
+  const float* ws1;  // gate_up: w3's
+  __nv_bfloat16* y;  // plain: [S, N]
+  const __nv_bfloat16* res;
+  uint8_t* hq;       // gate_up: [S, N] e4m3
+  float* hs;         // gate_up: [S, NB]
+  int act_kind;
+  float beta, lbeta;
+  int pow2;
+  int early;  // offsets were complete before the preceding kernel started
+  int probe;
+  DeviceStatus* st;
+};
+
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// Instruction descriptor: e4m3 x e4m3 -> fp32, both K-major.
+__device__ __forceinline__ uint32_t idesc_e4m3(int m, int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// tanh in fp32 to about 1e-6: its Taylor series below 0.25 (where 1 - 2/(e^2x + 1)
+// would cancel), that form above.
+__device__ __forceinline__ float tanh32(float x) {
+  const float x2 = x * x;
+  const float p =
+      x * (1.0f + x2 * (-1.0f / 3 + x2 * (2.0f / 15 + x2 * (-17.0f / 315 + x2 * (62.0f / 2835)))));
+  const float e = __expf(2.0f * fabsf(x));
+  const float t = copysignf(1.0f - __fdividef(2.0f, e + 1.0f), x);
+  return fabsf(x) < 0.25f ? p : t;
+}
+__device__ __forceinline__ float sigmoid32(float x) {
+  return __fdividef(1.0f, 1.0f + __expf(-x));
+}
+__device__ __forceinline__ float act32(float g, float u, int kind, float beta, float lbeta,
+                                       bool has_lb) {
+  if (kind == MOE_ACT_SITU) {
+    const float t = beta * tanh32(__fdividef(g, beta));
+    const float up = has_lb ? lbeta * tanh32(__fdividef(u, lbeta)) : u;
+    return t * sigmoid32(g) * up;
+  }
+  return g * sigmoid32(g) * u;
+}
+
+struct Unit {
+  int e, row0, nrows, nb;
+};
+
+template <int MODE, int BN, int TM, int STAGES>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_gemm_fp8(const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
+               const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA128,
+               const __grid_constant__ Args a) {
+  using C = Cfg<MODE, BN, TM, STAGES>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* tail = smem + STAGES * C::kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(tail);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + C::kBufs;
+  uint64_t* hmax = tempty + C::kBufs;  // gate_up: the two halves of a lane quarter met
+  uint64_t* never = hmax + 4;          // the diagnostics hook's (nothing arrives on it)
+  uint64_t* drain = never + 1;         // abort path: the MMAs issued have completed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* amax_x = reinterpret_cast<float*>(tail + kBarBytes);
+  int32_t* tile_start = reinterpret_cast<int32_t*>(tail + kBarBytes + C::kAmaxBytes);
+  static_assert((2 * STAGES + 2 * C::kBufs + 6) * 8 + 8 <= kBarBytes, "barriers");
+  __shared__ int32_t warp_tot[kThreads / 32];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int KB = (a.K + BK - 1) / BK;
+  const int NB = (a.N + 127) / 128;           // weight scale rows
+  constexpr int kUnitCols = MODE == kGateUp ? 128 : BN;  // output columns per unit
+  const int RB = (a.N + kUnitCols - 1) / kUnitCols;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < C::kBufs; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * C::kQuarters);
+    }
+    for (int q = 0; q < 4; ++q) mbar_init(&hmax[q], 2);
+    mbar_init(never, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    sm100::mbar_init_fence();
+  }
+  if (warp == kEpiWarps + 1) sm100::tmem_alloc(tmem_slot, kTmemCols);
+  if (!a.early) pdl_wait();
+
+  // Token tiles per segment and their prefix, by every CTA for itself: 4
+  // segments a thread.  A segment that is not inside [0, S] or runs backwards
+  // is recorded and gets no tile, so no row out of range is touched.
+  const int E = a.E;
+  {
+    const int e0 = 4 * threadIdx.x;
+    int32_t n[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      n[i] = 0;
+      if (e0 + i < E) {
+        const int64_t lo = a.offsets ? a.offsets[e0 + i] : 0;
+        const int64_t hi = a.offsets ? a.offsets[e0 + i + 1] : a.S;
+        const bool bad = lo < 0 || hi < lo || hi > a.S || (e0 + i == 0 && lo != 0);
+        if (!bad) n[i] = (int32_t)((hi - lo + TM - 1) / TM);
+        else if (blockIdx.x == 0) record_error(a.st, MOE_ERR_DEVICE_BOUNDS, 300);
+      }
+      sum += n[i];
+    }
+    int32_t x = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int32_t o = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += o;
+    }
+    if (lane == 31) warp_tot[warp] = x;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int32_t run = x - sum;
+    for (int w = 0; w < warp; ++w) run += warp_tot[w];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (e0 + i <= E && e0 + i <= kMaxSegments) tile_start[e0 + i] = run;
+      run += n[i];
+    }
+    __syncthreads();
+  }
+  const uint32_t tmem_base = *tmem_slot;
+  const int64_t total_units = (int64_t)tile_start[E] * RB;
+
+  auto unit_of = [&](int64_t u) {
+    Unit r;
+    const int tt = (int)(u / RB);
+    r.nb = (int)(u - (int64_t)tt * RB);
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {  // largest e with tile_start[e] <= tt
+      const int mid = (lo + hi + 1) >> 1;
+      if (tile_start[mid] <= tt) lo = mid;
+      else hi = mid - 1;
+    }
+    r.e = lo;
+    r.row0 = (a.offsets ? a.offsets[lo] : 0) + (tt - tile_start[lo]) * TM;
+    const int end = a.offsets ? a.offsets[lo + 1] : (int)a.S;
+    r.nrows = end - r.row0 < TM ? end - r.row0 : TM;
+    return r;
+  };
+
+  if (warp == kEpiWarps) {
+    // ------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int64_t filled = 0;  // stages handed to TMA so far
+      bool ok = true;
+      if (a.probe)  // the diagnostics hook: a wait that runs out
+        ok = mbar_wait(never, 0, abort_flag, kProbeLimitNs);
+      bool dep_pending = a.early != 0;
+      for (int64_t u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
+        const Unit w = unit_of(u);
+        const bool big = TM == 128 && w.nrows > 2 * kSmallBox;
+        const int nbox = big ? 1 : (w.nrows + kSmallBox - 1) / kSmallBox;
+        const uint32_t bytes = C::kBBytes + (big ? 128 : nbox * kSmallBox) * BK;
+        auto load_b = [&](int kb, int s) {
+          uint8_t* sB = smem + s * C::kStageBytes + C::kABytes;
+          if (MODE == kGateUp) {
+            tma_load_3d(&tmB0, &full[s], sB, kb * BK, w.nb * 128, w.e);
+            tma_load_3d(&tmB1, &full[s], sB + 128 * BK, kb * BK, w.nb * 128, w.e);
+          } else {
+#pragma unroll
+            for (int i = 0; i < BN / 128; ++i)
+              tma_load_3d(&tmB0, &full[s], sB + i * 128 * BK, kb * BK, w.nb * BN + i * 128, w.e);
+          }
+        };
+        auto load_a = [&](int kb, int s) {
+          uint8_t* sA = smem + s * C::kStageBytes;
+          if (big) {
+            tma_load_2d(&tmA128, &full[s], sA, kb * BK, w.row0);
+          } else {
+            for (int i = 0; i < nbox; ++i)
+              tma_load_2d(&tmA, &full[s], sA + i * kSmallBox * BK, kb * BK,
+                          w.row0 + i * kSmallBox);
+          }
+        };
+        int kb = 0;
+        if (dep_pending) {
+          // the weights of up to STAGES blocks first, then the wait for the
+          // kernel that writes the rows, then their rows
+          const int pre = KB < STAGES ? KB : STAGES;
+          for (; kb < pre; ++kb) {
+            if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
+            mbar_arrive_expect_tx(&full[stage], bytes);
+            load_b(kb, stage);
+            ++filled;
+            if (++stage == STAGES) { stage = 0; phase ^= 1; }
+          }
+          pdl_wait();
+          dep_pending = false;
+          for (int j = 0; j < kb; ++j) load_a(j, j);
+          if (!ok) break;
+        }
+        for (; kb < KB; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
+          mbar_arrive_expect_tx(&full[stage], bytes);
+          load_b(kb, stage);
+          load_a(kb, stage);
+          ++filled;
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        }
+      }
+      if (dep_pending) pdl_wait();
+      pdl_trigger();
+      if (!ok) {
+        record_error(a.st, MOE_ERR_DEVICE_TIMEOUT, 310 + MODE);
+        *abort_flag = 1;
+        volatile int go_on = 0;  // the CTA's copies in flight land before it ends
+        for (int64_t f = filled > STAGES ? filled - STAGES : 0; f < filled; ++f)
+          mbar_wait(&full[f % STAGES], (uint32_t)(f / STAGES) & 1, &go_on, kDrainNs);
+      }
+    }
+  } else if (warp == kEpiWarps + 1) {
+    // ------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, tphase = 0;
+      bool ok = true;
+      const uint32_t idesc = idesc_e4m3(BM, BN);
+      const uint64_t desc0 = sm100::smem_desc(smem_u32(smem), 1024, 2);
+      for (int64_t u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait(&tempty[buf], tphase ^ 1, abort_flag) ||
+              !mbar_wait(&full[stage], phase, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t da = desc0 + (uint64_t)(stage * (C::kStageBytes >> 4));
+          const uint64_t db = da + (uint64_t)(C::kABytes >> 4);
+          const uint32_t d = tmem_base + buf * BN;
+#pragma unroll
+          for (int k = 0; k < BK / UK; ++k)
+            umma_e4m3(d, da + (uint64_t)(k * UK / 16), db + (uint64_t)(k * UK / 16), idesc,
+                      k != 0);
+          umma_commit(&empty[stage]);
+          umma_commit(&tfull[buf]);
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+          if (++buf == C::kBufs) { buf = 0; tphase ^= 1; }
+        }
+      }
+      if (!ok) {
+        record_error(a.st, MOE_ERR_DEVICE_TIMEOUT, 320 + MODE);
+        *abort_flag = 1;
+        volatile int go_on = 0;
+        umma_commit(drain);
+        mbar_wait(drain, 0, &go_on, kDrainNs);
+      }
+    }
+  } else if ((warp & 3) < C::kQuarters) {
+    // ------------------------------------------------------ epilogue
+    const int quarter = warp & 3, half = warp >> 2;
+    constexpr int NC = BN / 2;  // columns per thread
+    const int row = quarter * 32 + lane;
+    const bool has_lb = !(a.lbeta == 0.0f || a.lbeta != a.lbeta);
+    const float b_eff = (a.beta == 0.0f || a.beta != a.beta) ? 1.0f : a.beta;
+    if (a.early) pdl_wait();
+    int buf = 0;
+    uint32_t tphase = 0, parity = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
+      const Unit w = unit_of(u);
+      const bool warp_live = quarter * 32 < w.nrows;
+      const bool live = row < w.nrows;
+      const int64_t grow = (int64_t)w.row0 + row;
+      // scales of K block b: the row's, and the one or two of the columns
+      const float* sxp = a.xs + (live ? grow : (int64_t)w.row0) * KB;
+      int sb = w.nb;
+      if (MODE == kPlain && BN == 256) sb = 2 * w.nb + half < NB ? 2 * w.nb + half : NB - 1;
+      const float* w0p = a.ws0 + ((int64_t)w.e * NB + sb) * KB;
+      const float* w1p = MODE == kGateUp ? a.ws1 + ((int64_t)w.e * NB + sb) * KB : nullptr;
+      float acc[NC];
+#pragma unroll
+      for (int i = 0; i < NC; ++i) acc[i] = 0.0f;
+      // scales are fetched kAhead blocks before their use
+      constexpr int kAhead = 4;
+      float sxr[kAhead], w0r[kAhead], w1r[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int b = j < KB ? j : KB - 1;
+        sxr[j] = __ldg(sxp + b);
+        w0r[j] = __ldg(w0p + b);
+        w1r[j] = MODE == kGateUp ? __ldg(w1p + b) : 0.0f;
+      }
+      for (int kb = 0; kb < KB; ++kb) {
+        const float c0 = sxr[0] * w0r[0], c1 = sxr[0] * w1r[0];
+#pragma unroll
+        for (int j = 0; j + 1 < kAhead; ++j) {
+          sxr[j] = sxr[j + 1];
+          w0r[j] = w0r[j + 1];
+          w1r[j] = w1r[j + 1];
+        }
+        const int b = kb + kAhead < KB ? kb + kAhead : KB - 1;
+        sxr[kAhead - 1] = __ldg(sxp + b);
+        w0r[kAhead - 1] = __ldg(w0p + b);
+        if (MODE == kGateUp) w1r[kAhead - 1] = __ldg(w1p + b);
+        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[buf], tphase, abort_flag))) {
+          if (lane == 0) record_error(a.st, MOE_ERR_DEVICE_TIMEOUT, 330 + MODE);
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (warp_live) {
+          const uint32_t t0 = tmem_base + ((uint32_t)(quarter * 32) << 16) + buf * BN;
+#pragma unroll
+          for (int c = 0; c < NC; c += 32) {
+            // gate_up: the thread's first 64 sums are g (w1), the next 64 u (w3)
+            const bool second = MODE == kGateUp && c >= 64;
+            const uint32_t col = MODE == kGateUp ? (second ? 128 : 0) + 64 * half + (c & 63)
+                                                 : half * NC + c;
+            uint32_t r[32];
+            sm100::tmem_ld32(t0 + col, r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              acc[c + i] = fmaf(__uint_as_float(r[i]), second ? c1 : c0, acc[c + i]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[buf]);
+        if (++buf == C::kBufs) { buf = 0; tphase ^= 1; }
+      }
+      if (!ok) break;
+      if (MODE == kPlain) {
+        const int n0 = w.nb * BN + half * NC;
+        __nv_bfloat16* dst = a.y + grow * a.N + n0;
+        const __nv_bfloat16* rsrc = a.res ? a.res + grow * a.N + n0 : nullptr;
+        if (live) {
+#pragma unroll
+          for (int c = 0; c < NC; c += 8) {
+            if (n0 + c < a.N) {  // N is a multiple of 8
+              float v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = acc[c + i];
+              if (rsrc) {
+                const uint4 t = *reinterpret_cast<const uint4*>(rsrc + c);
+                const uint32_t tw[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  v[2 * i] += __uint_as_float(tw[i] << 16);
+                  v[2 * i + 1] += __uint_as_float(tw[i] & 0xffff0000u);
+                }
+              }
+              uint32_t o[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                o[i] = *reinterpret_cast<const uint32_t*>(&p);
+              }
+              *reinterpret_cast<uint4*>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          }
+        }
+      } else {
+        // h of 64 columns in acc[0..63]; the block's largest |h| needs the
+        // other half's too: exchanged through shared memory (the buffer
+        // alternates, so a fast warp's next unit cannot overwrite it)
+        uint32_t m = 0;  // magnitudes as integers, NaN above infinity
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          acc[i] = act32(acc[i], acc[64 + i], a.act_kind, b_eff, a.lbeta, has_lb);
+          m = max(m, __float_as_uint(acc[i]) & 0x7fffffffu);
+        }
+        uint32_t* xch = reinterpret_cast<uint32_t*>(amax_x) + parity * 2 * BM;
+        xch[half * BM + row] = m;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&hmax[quarter]);
+        if (!__all_sync(0xffffffffu, mbar_wait(&hmax[quarter], parity, abort_flag))) {
+          if (lane == 0) record_error(a.st, MOE_ERR_DEVICE_TIMEOUT, 340);
+          *abort_flag = 1;
+          break;
+        }
+        m = max(m, xch[(half ^ 1) * BM + row]);
+        parity ^= 1;
+        float inv;
+        const float s = fp8::block_scale(__uint_as_float(m), a.pow2, inv);
+        const int f0 = w.nb * 128 + 64 * half;
+        if (live) {
+          uint8_t* dst = a.hq + grow * a.N + f0;
+#pragma unroll
+          for (int c = 0; c < 64; c += 16) {
+            if (f0 + c < a.N) {  // N is a multiple of 16
+              uint32_t o[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                o[i] = fp8::pack4(acc[c + 4 * i] * inv, acc[c + 4 * i + 1] * inv,
+                                  acc[c + 4 * i + 2] * inv, acc[c + 4 * i + 3] * inv);
+              *reinterpret_cast<uint4*>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          }
+          if (half == 0) a.hs[grow * NB + w.nb] = s;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kEpiWarps + 1) {
+    __syncwarp();
+    tc_fence_after();
+    sm100::tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------ tensor maps
+typedef CUresult (*EncodeTiledFn8)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn8 encode_8() {
+  static const EncodeTiledFn8 fn = [] {  // looked up once (thread-safe static)
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<EncodeTiledFn8>(p);
+    return static_cast<EncodeTiledFn8>(nullptr);
+  }();
+  return fn;
+}
+
+// [batch, rows, cols] bytes, box 128 columns x box_rows x 1, 128-byte swizzle;
+// what a box reaches beyond the tensor reads as zeros (e4m3 0), which the
+// products then ignore: K and N need not be multiples of 128.
+bool map_weights(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t batch) {
+  EncodeTiledFn8 fn = encode_8();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {cols, rows, batch};
+  cuuint64_t strides[2] = {cols, cols * rows};
+  cuuint32_t box[3] = {(cuuint32_t)BK, 128, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool map_rows(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows) {
+  EncodeTiledFn8 fn = encode_8();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols};
+  cuuint32_t box[2] = {(cuuint32_t)BK, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, int BN, int TM, int STAGES>
+cudaError_t launch(const CUtensorMap& b0, const CUtensorMap& b1, const CUtensorMap& a16,
+                   const CUtensorMap& a128, const Args& args, cudaStream_t s) {
+  using C = Cfg<MODE, BN, TM, STAGES>;
+  constexpr auto kernel = k_gemm_fp8<MODE, BN, TM, STAGES>;
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t set_up[kMaxDevices];
+  const cudaError_t e = once_per_device(once, set_up, [&](int) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)C::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  // no more CTAs than units: at most one token tile per TM rows and segment
+  const int cols = MODE == kGateUp ? 128 : BN;
+  const int64_t tiles = args.S / TM + (args.S < args.E ? args.S : args.E);
+  const int64_t units = tiles * ((args.N + cols - 1) / cols);
+  const int sms = dev_info()->sm_count;
+  return launch_pdl(kernel, dim3((unsigned)(units < sms ? units : sms)), dim3(kThreads), C::kSmem,
+                    s, b0, b1, a16, a128, args);
+}
+
+template <int MODE>
+cudaError_t launch_variant(const CUtensorMap& b0, const CUtensorMap& b1, const CUtensorMap& a16,
+                           const CUtensorMap& a128, const Args& args, cudaStream_t s) {
+  if (args.S <= 16 * (int64_t)args.E) {
+    if constexpr (MODE == kGateUp) return launch<MODE, 256, 32, 6>(b0, b1, a16, a128, args, s);
+    else return launch<MODE, 128, 32, 10>(b0, b1, a16, a128, args, s);
+  }
+  return launch<MODE, 256, 128, 4>(b0, b1, a16, a128, args, s);
+}
+
+}  // namespace
+
+int grouped_fp8_run(const uint8_t* xq, const float* xs, const int32_t* offsets, int E, int64_t S,
+                    int K, const uint8_t* w, const float* ws, int N, const __nv_bfloat16* residual,
+                    __nv_bfloat16* y, DeviceStatus* st, cudaStream_t s, bool early) {
+  CUtensorMap mw, m16, m128;
+  if (!map_weights(&mw, w, K, N, E) || !map_rows(&m16, xq, K, S, kSmallBox) ||
+      !map_rows(&m128, xq, K, S, 128))
+    return MOE_ERR_CUDA;
+  Args a{};
+  a.offsets = offsets;
+  a.E = E;
+  a.S = S;
+  a.N = N;
+  a.K = K;
+  a.xs = xs;
+  a.ws0 = ws;
+  a.y = y;
+  a.res = residual;
+  a.early = early ? 1 : 0;
+  a.probe = wait_probe();
+  a.st = st;
+  return launch_variant<kPlain>(mw, mw, m16, m128, a, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+size_t expert_fp8_scratch_bytes(int64_t S, int F) {
+  return align_up((size_t)S * (size_t)F, 256) +
+         align_up(sizeof(float) * (size_t)S * (size_t)((F + 127) / 128), 256);
+}
+
+int expert_ffn_fp8_run(const uint8_t* xq, const float* xs, const int32_t* offsets, int E, int64_t S,
+                       int d, int F, const uint8_t* w1, const float* w1s, const uint8_t* w3,
+                       const float* w3s, const uint8_t* w2, const float* w2s,
+                       const moe_act_cfg& act, bool pow2, __nv_bfloat16* y, void* scratch,
+                       DeviceStatus* st, cudaStream_t s) {
+  uint8_t* hq = static_cast<uint8_t*>(scratch);
+  float* hs = reinterpret_cast<float*>(hq + align_up((size_t)S * (size_t)F, 256));
+  CUtensorMap mw1, mw3, m16, m128;
+  if (!map_weights(&mw1, w1, d, F, E) || !map_weights(&mw3, w3, d, F, E) ||
+      !map_rows(&m16, xq, d, S, kSmallBox) || !map_rows(&m128, xq, d, S, 128))
+    return MOE_ERR_CUDA;
+  Args a{};
+  a.offsets = offsets;
+  a.E = E;
+  a.S = S;
+  a.N = F;
+  a.K = d;
+  a.xs = xs;
+  a.ws0 = w1s;
+  a.ws1 = w3s;
+  a.hq = hq;
+  a.hs = hs;
+  a.act_kind = act.kind;
+  a.beta = act.beta;
+  a.lbeta = act.linear_beta;
+  a.pow2 = pow2 ? 1 : 0;
+  a.probe = wait_probe();
+  a.st = st;
+  if (launch_variant<kGateUp>(mw1, mw3, m16, m128, a, s) != cudaSuccess) return MOE_ERR_CUDA;
+  // offsets were read by the kernel just launched, after its own wait: the
+  // down kernel may read them, and fetch weights, before that kernel ends
+  return grouped_fp8_run(hq, hs, offsets, E, S, F, w2, w2s, d, nullptr, y, st, s, true);
+}
+
+}  // namespace moe

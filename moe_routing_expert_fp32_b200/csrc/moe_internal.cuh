@@ -203,6 +203,33 @@ cudaError_t launch_ep_combine_rows(const PeerTable& pt, const int32_t* pos,
                                    int K, int d, __nv_bfloat16* out, DeviceStatus* st,
                                    cudaStream_t s);
 
+// quantize_fp8.cu: bf16 to e4m3 with fp32 block scales.
+// pos (optional): row t is stored at the top_k rows pos[t * top_k + k] < S
+cudaError_t launch_quantize_rows(const __nv_bfloat16* x, int64_t M, int K, bool pow2, uint8_t* q,
+                                 float* scale, const int32_t* pos, int top_k, int64_t S,
+                                 cudaStream_t s);
+cudaError_t launch_quantize_blocks(const __nv_bfloat16* x, int64_t B, int64_t M, int K, bool pow2,
+                                   uint8_t* q, float* scale, cudaStream_t s);
+
+// gemm_fp8.cu: products of 8-bit block-scaled operands.
+// offsets [E + 1], or nullptr with E = 1: one segment of all S rows.
+// early: offsets were complete before the kernel preceding on `s` started.
+int grouped_fp8_run(const uint8_t* xq, const float* xs, const int32_t* offsets, int E, int64_t S,
+                    int K, const uint8_t* w, const float* ws, int N, const __nv_bfloat16* residual,
+                    __nv_bfloat16* y, DeviceStatus* st, cudaStream_t s, bool early);
+// h [S, F] e4m3 and its scales [S, ceil(F / 128)]
+size_t expert_fp8_scratch_bytes(int64_t S, int F);
+int expert_ffn_fp8_run(const uint8_t* xq, const float* xs, const int32_t* offsets, int E, int64_t S,
+                       int d, int F, const uint8_t* w1, const float* w1s, const uint8_t* w3,
+                       const float* w3s, const uint8_t* w2, const float* w2s,
+                       const moe_act_cfg& act, bool pow2, __nv_bfloat16* y, void* scratch,
+                       DeviceStatus* st, cudaStream_t s);
+
+// The diagnostics hook's switch (moe_set_wait_probe), read at every launch,
+// and the limit of the wait that it makes run out.
+int wait_probe();
+constexpr uint64_t kProbeLimitNs = 1000000ull;
+
 // device properties, read once per device
 struct DevInfo {
   int sm_count;
