@@ -48,7 +48,11 @@ constexpr int BM = 128;        // MMA M: token rows
 constexpr int BK = 128;        // K per stage = scale block = one 128-byte swizzle row
 constexpr int UK = 32;         // K per tcgen05.mma for 8-bit inputs
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (kEpiWarps + 2);  // + TMA warp, MMA warp
+constexpr int kThreads = 32 * (kEpiWarps + 4);  // + TMA warp, MMA warp, two idle (whole warpgroups)
+// Registers per thread after the split of the launch's 168 x 384: the epilogue
+// holds 128 sums and a 32-column TMEM load, the other warpgroup next to nothing.
+constexpr int kEpiRegs = 216, kCtlRegs = 72;
+static_assert(kEpiRegs * 32 * kEpiWarps + kCtlRegs * 128 <= 168 * kThreads, "register split");
 constexpr int kTmemCols = 512;
 constexpr int kSmallBox = 16;  // token rows per small TMA box
 constexpr int kMaxSegments = 1024;
@@ -109,6 +113,21 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, ui
 __device__ __forceinline__ uint32_t idesc_e4m3(int m, int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
+
+// (acc.x, acc.y) += (lo, hi) * (c.x, c.y), each rounded once: one instruction
+// for two sums.
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t c) {
+  asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}"
+      : "+l"(acc)
+      : "r"(lo), "r"(hi), "l"(c));
+}
+__device__ __forceinline__ uint64_t pair_of(float v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
 // tanh in fp32 to about 1e-6: its Taylor series below 0.25 (where 1 - 2/(e^2x + 1)
 // would cancel), that form above.
@@ -243,6 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     return r;
   };
 
+  if (warp >= kEpiWarps) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
   if (warp == kEpiWarps) {
     // ------------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -352,7 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(drain, 0, &go_on, kDrainNs);
       }
     }
-  } else if ((warp & 3) < C::kQuarters) {
+  }
+  } else {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+  if ((warp & 3) < C::kQuarters) {
     // ------------------------------------------------------ epilogue
     const int quarter = warp & 3, half = warp >> 2;
     constexpr int NC = BN / 2;  // columns per thread
@@ -374,9 +398,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (MODE == kPlain && BN == 256) sb = 2 * w.nb + half < NB ? 2 * w.nb + half : NB - 1;
       const float* w0p = a.ws0 + ((int64_t)w.e * NB + sb) * KB;
       const float* w1p = MODE == kGateUp ? a.ws1 + ((int64_t)w.e * NB + sb) * KB : nullptr;
-      float acc[NC];
+      uint64_t acc2[NC / 2];  // the sums of columns 2i and 2i + 1
 #pragma unroll
-      for (int i = 0; i < NC; ++i) acc[i] = 0.0f;
+      for (int i = 0; i < NC / 2; ++i) acc2[i] = 0;
       // scales are fetched kAhead blocks before their use
       constexpr int kAhead = 4;
       float sxr[kAhead], w0r[kAhead], w1r[kAhead];
@@ -388,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         w1r[j] = MODE == kGateUp ? __ldg(w1p + b) : 0.0f;
       }
       for (int kb = 0; kb < KB; ++kb) {
-        const float c0 = sxr[0] * w0r[0], c1 = sxr[0] * w1r[0];
+        const uint64_t c0 = pair_of(sxr[0] * w0r[0]), c1 = pair_of(sxr[0] * w1r[0]);
 #pragma unroll
         for (int j = 0; j + 1 < kAhead; ++j) {
           sxr[j] = sxr[j + 1];
@@ -417,8 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t r[32];
             sm100::tmem_ld32(t0 + col, r);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              acc[c + i] = fmaf(__uint_as_float(r[i]), second ? c1 : c0, acc[c + i]);
+            for (int i = 0; i < 16; ++i)
+              fma2(acc2[c / 2 + i], r[2 * i], r[2 * i + 1], second ? c1 : c0);
           }
         }
         tc_fence_before();
@@ -427,6 +451,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++buf == C::kBufs) { buf = 0; tphase ^= 1; }
       }
       if (!ok) break;
+      float acc[NC];
+#pragma unroll
+      for (int i = 0; i < NC / 2; ++i) {
+        acc[2 * i] = lo_of(acc2[i]);
+        acc[2 * i + 1] = hi_of(acc2[i]);
+      }
       if (MODE == kPlain) {
         const int n0 = w.nb * BN + half * NC;
         __nv_bfloat16* dst = a.y + grow * a.N + n0;
@@ -499,6 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  }  // roles
   tc_fence_before();
   __syncthreads();
   if (warp == kEpiWarps + 1) {
