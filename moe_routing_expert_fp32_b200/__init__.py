@@ -11,7 +11,6 @@ binding's functions raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -654,35 +653,45 @@ def block_forward(x, weights: BlockWeights, cfg: RouteConfig, act: ActConfig, no
 
 
 # ------------------------------------------------- 8-bit block-scaled forms
+# These calls take a few microseconds on the GPU at decode sizes, so the
+# marshalling is kept short: raw pointers, the raw stream, one pass of checks.
 def _fp8_args(*named):
     """Checks (name, tensor, dtype, shape) entries: contiguous CUDA tensors of one
-    device, of that dtype and shape (None: any).  Returns the device."""
-    dev = named[0][1].device
+    device, of that dtype and shape (None: any).  Returns the device's index."""
+    dev = named[0][1].get_device()
     for name, t, dtype, shape in named:
-        if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
         if shape is not None and t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, {named[0][0]} on {dev}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, {named[0][0]} on cuda:{dev}")
     return dev
 
 
-def _on(dev):
-    """Makes `dev` current for the calls inside, when it is not already."""
-    torch = _torch()
-    if torch.cuda.current_device() == dev.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+def _fp8_call(fn: str, dev: int, *args):
+    """Calls fn(*args, stream) on the current stream of device `dev`, which is made
+    current for the call when it is not."""
+    C = _torch()._C
+    if C._cuda_getDevice() == dev:
+        code = getattr(lib(), fn)(*args, C._cuda_getCurrentRawStream(dev))
+    else:
+        with _torch().cuda.device(dev):
+            code = getattr(lib(), fn)(*args, C._cuda_getCurrentRawStream(dev))
+    _check(fn, code)
 
 
 def _ws_for(ws, need, dev):
-    torch = _torch()
     if ws is None:
+        torch = _torch()
         return torch.empty(need, dtype=torch.uint8, device=dev)
-    if ws.device != dev:
-        raise ValueError(f"ws is on {ws.device}, expected {dev}")
+    if ws.get_device() != dev:
+        raise ValueError(f"ws is on {ws.device}, expected cuda:{dev}")
     return ws
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
 
 
 def _c128(n):
@@ -718,10 +727,8 @@ def quantize_fp8(x, block_rows: int = 1, pow2_scales: bool = False, q=None, scal
     dev = _fp8_args(*named)
     q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev) if q is None else q
     scale = torch.empty(s_shape, dtype=torch.float32, device=dev) if scale is None else scale
-    with _on(dev):
-        _check("moe_quantize_fp8",
-               lib().moe_quantize_fp8(_ptr(x), B, M, K, block_rows, int(pow2_scales), _ptr(q),
-                                      _ptr(scale), _stream()))
+    _fp8_call("moe_quantize_fp8", dev, x.data_ptr(), B, M, K, block_rows, int(pow2_scales),
+              q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
@@ -743,11 +750,9 @@ def dispatch_fp8(topk_idx, x_e, num_experts: int, pow2_scales: bool = False, ws=
     xq = torch.empty((S, d_e), dtype=torch.float8_e4m3fn, device=dev)
     xs = torch.empty((S, _c128(d_e)), dtype=torch.float32, device=dev)
     ws = _ws_for(ws, lib().moe_dispatch_workspace_size(N, K, E), dev)
-    with _on(dev):
-        _check("moe_dispatch_fp8",
-               lib().moe_dispatch_fp8(_ptr(topk_idx), N, K, E, _ptr(x_e), d_e, int(pow2_scales),
-                                      _ptr(counts), _ptr(offsets), _ptr(perm), _ptr(pos),
-                                      _ptr(xq), _ptr(xs), _ptr(ws), ws.numel(), _stream()))
+    _fp8_call("moe_dispatch_fp8", dev, topk_idx.data_ptr(), N, K, E, x_e.data_ptr(), d_e,
+              int(pow2_scales), counts.data_ptr(), offsets.data_ptr(), perm.data_ptr(),
+              pos.data_ptr(), xq.data_ptr(), xs.data_ptr(), ws.data_ptr(), ws.numel())
     return counts, offsets, perm, pos, xq, xs
 
 
@@ -766,15 +771,10 @@ def linear_fp8(xq, x_scale, w, w_scale, residual=None, out=None, ws=None):
     if out is not None:
         named.append(("out", out, bf, (M, N)))
     dev = _fp8_args(*named)
-    need = lib().moe_linear_fp8_workspace_size(M, K, N)
-    if need == 0:
-        raise MoeError("moe_linear_fp8_workspace_size", -2)
-    ws = _ws_for(ws, need, dev)
+    ws = _ws_for(ws, 256, dev)  # moe_linear_fp8_workspace_size: the status word
     out = torch.empty((M, N), dtype=bf, device=dev) if out is None else out
-    with _on(dev):
-        _check("moe_linear_fp8",
-               lib().moe_linear_fp8(_ptr(xq), _ptr(x_scale), M, K, _ptr(w), _ptr(w_scale), N,
-                                    _ptr(residual), _ptr(out), _ptr(ws), ws.numel(), _stream()))
+    _fp8_call("moe_linear_fp8", dev, xq.data_ptr(), x_scale.data_ptr(), M, K, w.data_ptr(),
+              w_scale.data_ptr(), N, _opt(residual), out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 
@@ -793,16 +793,11 @@ def grouped_linear_fp8(xq, x_scale, offsets, w, w_scale, out=None, ws=None):
     if out is not None:
         named.append(("out", out, bf, (S, N)))
     dev = _fp8_args(*named)
-    need = lib().moe_grouped_linear_fp8_workspace_size(S, K, E, N)
-    if need == 0:
-        raise MoeError("moe_grouped_linear_fp8_workspace_size", -2)
-    ws = _ws_for(ws, need, dev)
+    ws = _ws_for(ws, 256, dev)  # moe_grouped_linear_fp8_workspace_size: the status word
     out = torch.empty((S, N), dtype=bf, device=dev) if out is None else out
-    with _on(dev):
-        _check("moe_grouped_linear_fp8",
-               lib().moe_grouped_linear_fp8(_ptr(xq), _ptr(x_scale), _ptr(offsets), E, S, K,
-                                            _ptr(w), _ptr(w_scale), N, _ptr(out), _ptr(ws),
-                                            ws.numel(), _stream()))
+    _fp8_call("moe_grouped_linear_fp8", dev, xq.data_ptr(), x_scale.data_ptr(),
+              offsets.data_ptr(), E, S, K, w.data_ptr(), w_scale.data_ptr(), N, out.data_ptr(),
+              ws.data_ptr(), ws.numel())
     return out
 
 
@@ -839,11 +834,9 @@ def expert_ffn_fp8(xq, x_scale, offsets, w1, w1_scale, w3, w3_scale, w2, w2_scal
     ws = _ws_for(ws, need, dev)
     y = torch.empty((S, d), dtype=torch.bfloat16, device=dev) if y is None else y
     a = act._c()
-    with _on(dev):
-        _check("moe_expert_ffn_fp8",
-               lib().moe_expert_ffn_fp8(_ptr(xq), _ptr(x_scale), _ptr(offsets), E, S, d, F,
-                                        ctypes.byref(xw), ctypes.byref(a), int(pow2_scales),
-                                        _ptr(y), _ptr(ws), ws.numel(), _stream()))
+    _fp8_call("moe_expert_ffn_fp8", dev, xq.data_ptr(), x_scale.data_ptr(), offsets.data_ptr(), E,
+              S, d, F, ctypes.byref(xw), ctypes.byref(a), int(pow2_scales), y.data_ptr(),
+              ws.data_ptr(), ws.numel())
     return y
 
 
@@ -876,10 +869,8 @@ def forward_fp8(x_r, W, bias, cfg: RouteConfig, w1, w1_scale, w3, w3_scale, w2, 
         raise MoeError("moe_forward_fp8_workspace_size", -2)
     ws = _ws_for(ws, need, dev)
     out = torch.empty((N, d_e), dtype=torch.bfloat16, device=dev) if out is None else out
-    with _on(dev):
-        _check("moe_forward_fp8",
-               lib().moe_forward_fp8(_ptr(x_r), _ptr(x_e), N, d_r, d_e, _ptr(W), _ptr(bias),
-                                     ctypes.byref(c), ctypes.byref(xw), F, ctypes.byref(a),
-                                     int(pow2_scales), _ptr(out), _ptr(topk_idx), _ptr(topk_w),
-                                     _ptr(ws), ws.numel(), _stream()))
+    _fp8_call("moe_forward_fp8", dev, x_r.data_ptr(), _opt(x_e), N, d_r, d_e, W.data_ptr(),
+              _opt(bias), ctypes.byref(c), ctypes.byref(xw), F, ctypes.byref(a),
+              int(pow2_scales), out.data_ptr(), _opt(topk_idx), _opt(topk_w), ws.data_ptr(),
+              ws.numel())
     return out

@@ -711,10 +711,9 @@ int moe_grouped_linear_fp8(const moe_fp8* xq, const float* x_scale, const int32_
     return rc;
   if ((rc = check_device())) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((rc = reset_status(ws, s))) return rc;
-  if (S == 0) return MOE_OK;
+  if (S == 0) return reset_status(ws, s);
   return grouped_fp8_run(xq, x_scale, offsets, E, S, K, w, w_scale, N_out, nullptr,
-                         reinterpret_cast<__nv_bfloat16*>(y), status_of(ws), s, false);
+                         reinterpret_cast<__nv_bfloat16*>(y), status_of(ws), s, false, true);
 }
 
 size_t moe_linear_fp8_workspace_size(int64_t M, int K, int N_out) {
@@ -731,11 +730,10 @@ int moe_linear_fp8(const moe_fp8* xq, const float* x_scale, int64_t M, int K, co
   if ((rc = check_ws(ws, ws_bytes, moe_linear_fp8_workspace_size(M, K, N_out)))) return rc;
   if ((rc = check_device())) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((rc = reset_status(ws, s))) return rc;
-  if (M == 0) return MOE_OK;
+  if (M == 0) return reset_status(ws, s);
   return grouped_fp8_run(xq, x_scale, nullptr, 1, M, K, w, w_scale, N_out,
                          reinterpret_cast<const __nv_bfloat16*>(residual),
-                         reinterpret_cast<__nv_bfloat16*>(y), status_of(ws), s, false);
+                         reinterpret_cast<__nv_bfloat16*>(y), status_of(ws), s, false, true);
 }
 
 namespace {
@@ -768,11 +766,11 @@ int moe_expert_ffn_fp8(const moe_fp8* xq, const float* x_scale, const int32_t* o
   if ((rc = check_ws(ws, ws_bytes, moe_expert_ffn_fp8_workspace_size(S, d_e, E, F)))) return rc;
   if ((rc = check_device())) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((rc = reset_status(ws, s))) return rc;
-  if (S == 0) return MOE_OK;
+  if (S == 0) return reset_status(ws, s);
   return expert_ffn_fp8_run(xq, x_scale, offsets, E, S, d_e, F, w->w1, w->w1_scale, w->w3,
                             w->w3_scale, w->w2, w->w2_scale, *act, pow2_scales != 0,
-                            reinterpret_cast<__nv_bfloat16*>(y), body_of(ws), status_of(ws), s);
+                            reinterpret_cast<__nv_bfloat16*>(y), body_of(ws), status_of(ws), s,
+                            true);
 }
 
 namespace {
@@ -877,7 +875,8 @@ int moe_forward_fp8(const moe_bf16* x_r, const moe_bf16* x_e, int64_t N, int d_r
     const Range r("moe.expert_ffn_fp8");
     if ((rc = expert_ffn_fp8_run(xq, xs, offsets, E, N * K, d_e, F, experts->w1,
                                  experts->w1_scale, experts->w3, experts->w3_scale, experts->w2,
-                                 experts->w2_scale, *act, pow2_scales != 0, y, stage, st, s)))
+                                 experts->w2_scale, *act, pow2_scales != 0, y, stage, st, s,
+                                 false)))
       return rc;
   }
   const Range r("moe.combine");

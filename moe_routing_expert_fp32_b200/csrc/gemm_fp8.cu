@@ -17,9 +17,7 @@
 // 128-column block is a maximum over its own registers (and one neighbour's).
 //   * gate_up: the N side is 128 rows of w1 over the same 128 rows of w3, so a
 //     unit yields whole 128-column blocks of h, which it rounds to e4m3 itself;
-//   * M is 128 rows whatever the segment: a decode tile (TM = 32) loads only its
-//     rows and lets the MMA read on into the weights behind them, which fills
-//     accumulator lanes that nothing reads.
+//   * few rows per segment: k_gemm_fp8_dec turns the sides round.
 // Roles: 8 epilogue warps (lane quarter = warp % 4, column half = warp / 4), one
 // TMA warp, one MMA warp; a ring of stages guarded by mbarriers; a persistent
 // grid over units (token tile, weight block), weight block fastest.  Every wait
@@ -63,19 +61,17 @@ constexpr uint64_t kDrainNs = 100000000ull;
 
 enum Mode { kPlain = 0, kGateUp = 1 };
 
-template <int MODE, int BN, int TM, int STAGES>
+template <int MODE, int BN, int STAGES>
 struct Cfg {
-  static constexpr int kABytes = TM * BK;
+  static constexpr int kABytes = BM * BK;
   static constexpr int kBBytes = BN * BK;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kBufs = kTmemCols / BN;
-  static constexpr int kQuarters = TM / 32;  // lane quarters that can hold rows
   static constexpr int kStartBytes = (kMaxSegments + 1) * 4;
   static constexpr int kAmaxBytes = 2 * 2 * BM * 4;  // unit parity x half x row
   static constexpr size_t kSmem = (size_t)STAGES * kStageBytes + 1024 + kBarBytes +
                                   kAmaxBytes + kStartBytes;
   static_assert(kABytes % 1024 == 0 && kBBytes % 1024 == 0, "1024-byte aligned operands");
-  static_assert(kStageBytes >= BM * BK, "the MMA's 128 A rows stay inside the ring");
   static_assert(MODE == kPlain || BN == 256, "gate_up: 128 rows of w1 and of w3");
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -97,6 +93,7 @@ struct Args {
   float beta, lbeta;
   int pow2;
   int early;  // offsets were complete before the preceding kernel started
+  int reset;  // the first kernel of its call: it clears the status word
   int probe;
   DeviceStatus* st;
 };
@@ -108,6 +105,9 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, ui
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 // Instruction descriptor: e4m3 x e4m3 -> fp32, both K-major.
 __device__ __forceinline__ uint32_t idesc_e4m3(int m, int n) {
@@ -152,16 +152,82 @@ __device__ __forceinline__ float act32(float g, float u, int kind, float beta, f
   return g * sigmoid32(g) * u;
 }
 
+// Token tiles of `tile` rows per segment and their prefix into tile_start
+// [E + 1] (shared memory), by every CTA for itself.  A segment that is not
+// inside [0, S] or runs backwards is recorded and gets no tile, so no row out
+// of range is touched.  Every thread of the CTA calls it, after the wait on the
+// kernel before; it ends with a __syncthreads.
+template <int THREADS>
+__device__ __forceinline__ void build_tiles(const Args& a, int tile, int32_t* tile_start,
+                                            int32_t* warp_tot) {
+  constexpr int kPer = (kMaxSegments + THREADS) / THREADS;  // segments per thread, and E itself
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int e0 = kPer * threadIdx.x;
+  if (a.reset && blockIdx.x == 0) {
+    // instead of a memset before the kernel; the other CTAs record nothing but
+    // waits that have run out, long after this
+    if (threadIdx.x == 0) *a.st = DeviceStatus{0, 0};
+    __syncthreads();
+  }
+  int32_t n[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    n[i] = 0;
+    if (e0 + i < a.E) {
+      const int64_t lo = a.offsets ? a.offsets[e0 + i] : 0;
+      const int64_t hi = a.offsets ? a.offsets[e0 + i + 1] : a.S;
+      const bool bad = lo < 0 || hi < lo || hi > a.S || (e0 + i == 0 && lo != 0);
+      if (!bad) n[i] = (int32_t)((hi - lo + tile - 1) / tile);
+      else if (blockIdx.x == 0) record_error(a.st, MOE_ERR_DEVICE_BOUNDS, 300);
+    }
+    sum += n[i];
+  }
+  int32_t x = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int32_t o = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += o;
+  }
+  if (lane == 31) warp_tot[warp] = x;
+  __syncthreads();
+  int32_t run = x - sum;
+  for (int w = 0; w < warp; ++w) run += warp_tot[w];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (e0 + i <= a.E) tile_start[e0 + i] = run;
+    run += n[i];
+  }
+  __syncthreads();
+}
+
 struct Unit {
   int e, row0, nrows, nb;
 };
+// Unit u: weight block u % RB of token tile u / RB.
+__device__ __forceinline__ Unit unit_at(const Args& a, const int32_t* tile_start, int RB, int tile,
+                                        int64_t u) {
+  Unit r;
+  const int tt = (int)(u / RB);
+  r.nb = (int)(u - (int64_t)tt * RB);
+  int lo = 0, hi = a.E - 1;
+  while (lo < hi) {  // largest e with tile_start[e] <= tt
+    const int mid = (lo + hi + 1) >> 1;
+    if (tile_start[mid] <= tt) lo = mid;
+    else hi = mid - 1;
+  }
+  r.e = lo;
+  r.row0 = (a.offsets ? a.offsets[lo] : 0) + (tt - tile_start[lo]) * tile;
+  const int end = a.offsets ? a.offsets[lo + 1] : (int)a.S;
+  r.nrows = end - r.row0 < tile ? end - r.row0 : tile;
+  return r;
+}
 
-template <int MODE, int BN, int TM, int STAGES>
+template <int MODE, int BN, int STAGES>
 __global__ void __launch_bounds__(kThreads, 1)
     k_gemm_fp8(const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
                const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA128,
                const __grid_constant__ Args a) {
-  using C = Cfg<MODE, BN, TM, STAGES>;
+  using C = Cfg<MODE, BN, STAGES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -193,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < C::kBufs; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 2 * C::kQuarters);
+      mbar_init(&tempty[b], kEpiWarps);
     }
     for (int q = 0; q < 4; ++q) mbar_init(&hmax[q], 2);
     mbar_init(never, 1);
@@ -201,66 +267,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     sm100::mbar_init_fence();
   }
+  if (warp == kEpiWarps && lane == 0) {
+    prefetch_map(&tmB0);
+    prefetch_map(&tmA);
+    prefetch_map(&tmA128);
+    if (MODE == kGateUp) prefetch_map(&tmB1);
+  }
   if (warp == kEpiWarps + 1) sm100::tmem_alloc(tmem_slot, kTmemCols);
   if (!a.early) pdl_wait();
 
-  // Token tiles per segment and their prefix, by every CTA for itself: 4
-  // segments a thread.  A segment that is not inside [0, S] or runs backwards
-  // is recorded and gets no tile, so no row out of range is touched.
-  const int E = a.E;
-  {
-    const int e0 = 4 * threadIdx.x;
-    int32_t n[4], sum = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      n[i] = 0;
-      if (e0 + i < E) {
-        const int64_t lo = a.offsets ? a.offsets[e0 + i] : 0;
-        const int64_t hi = a.offsets ? a.offsets[e0 + i + 1] : a.S;
-        const bool bad = lo < 0 || hi < lo || hi > a.S || (e0 + i == 0 && lo != 0);
-        if (!bad) n[i] = (int32_t)((hi - lo + TM - 1) / TM);
-        else if (blockIdx.x == 0) record_error(a.st, MOE_ERR_DEVICE_BOUNDS, 300);
-      }
-      sum += n[i];
-    }
-    int32_t x = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int32_t o = __shfl_up_sync(0xffffffffu, x, off);
-      if (lane >= off) x += o;
-    }
-    if (lane == 31) warp_tot[warp] = x;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    int32_t run = x - sum;
-    for (int w = 0; w < warp; ++w) run += warp_tot[w];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (e0 + i <= E && e0 + i <= kMaxSegments) tile_start[e0 + i] = run;
-      run += n[i];
-    }
-    __syncthreads();
-  }
+  tc_fence_before();
+  build_tiles<kThreads>(a, BM, tile_start, warp_tot);
+  tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int64_t total_units = (int64_t)tile_start[E] * RB;
+  const int64_t total_units = (int64_t)tile_start[a.E] * RB;
 
-  auto unit_of = [&](int64_t u) {
-    Unit r;
-    const int tt = (int)(u / RB);
-    r.nb = (int)(u - (int64_t)tt * RB);
-    int lo = 0, hi = E - 1;
-    while (lo < hi) {  // largest e with tile_start[e] <= tt
-      const int mid = (lo + hi + 1) >> 1;
-      if (tile_start[mid] <= tt) lo = mid;
-      else hi = mid - 1;
-    }
-    r.e = lo;
-    r.row0 = (a.offsets ? a.offsets[lo] : 0) + (tt - tile_start[lo]) * TM;
-    const int end = a.offsets ? a.offsets[lo + 1] : (int)a.S;
-    r.nrows = end - r.row0 < TM ? end - r.row0 : TM;
-    return r;
-  };
+  auto unit_of = [&](int64_t u) { return unit_at(a, tile_start, RB, BM, u); };
 
   if (warp >= kEpiWarps) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
@@ -276,9 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool dep_pending = a.early != 0;
       for (int64_t u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
         const Unit w = unit_of(u);
-        const bool big = TM == 128 && w.nrows > 2 * kSmallBox;
+        const bool big = w.nrows > 2 * kSmallBox;
         const int nbox = big ? 1 : (w.nrows + kSmallBox - 1) / kSmallBox;
-        const uint32_t bytes = C::kBBytes + (big ? 128 : nbox * kSmallBox) * BK;
+        const uint32_t bytes = C::kBBytes + (big ? BM : nbox * kSmallBox) * BK;
         auto load_b = [&](int kb, int s) {
           uint8_t* sB = smem + s * C::kStageBytes + C::kABytes;
           if (MODE == kGateUp) {
@@ -304,8 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (dep_pending) {
           // the weights of up to STAGES blocks first, then the wait for the
           // kernel that writes the rows, then their rows
-          const int pre = KB < STAGES ? KB : STAGES;
-          for (; kb < pre; ++kb) {
+          for (; kb < STAGES && kb < KB; ++kb) {
             if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
             mbar_arrive_expect_tx(&full[stage], bytes);
             load_b(kb, stage);
@@ -376,7 +397,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   } else {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
-  if ((warp & 3) < C::kQuarters) {
     // ------------------------------------------------------ epilogue
     const int quarter = warp & 3, half = warp >> 2;
     constexpr int NC = BN / 2;  // columns per thread
@@ -528,7 +548,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  }
   }  // roles
   tc_fence_before();
   __syncthreads();
@@ -536,6 +555,416 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_after();
     sm100::tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+// --------------------------------------------------------- decode variant
+// A few rows per segment: the product is a stream of weights.  Here the weight
+// rows are the MMA's M side (128 of them; gate_up 128 of w1 and the same 128 of
+// w3, each with its accumulator) and up to 32 token rows its N side, rounded up
+// to 16, so an MMA costs little more than reading the weights from shared
+// memory, and a K block leaves 16 or 32 sums per thread to add instead of 128.
+// (With the token rows on the M side a stream of 8-bit weights ran at 4.9-5.4
+// TB/s, paced by the MMAs on 128 mostly empty rows and by the two epilogue
+// warps that hold the 32 rows; the loads alone reach 7.)
+// The row scales then differ by column: each epilogue warp forms its 32 products
+// sx * sw, one per lane, and passes them round through shared memory.
+// A stage holds KSUB K blocks, so that 256 contiguous bytes of a weight row are
+// asked for together.
+// SPLIT: a cluster of 2, 4 or 8 CTAs shares a unit, each takes a part of K,
+// and the parts are added in rank order through distributed shared memory:
+// for a Linear of few rows, whose units alone would leave most SMs idle.  Every
+// cluster has one unit at most.
+constexpr int kNt = 32;         // token rows per tile
+constexpr int kDecThreads = 192;  // warps 0-3 epilogue, 4 TMA, 5 MMA
+
+template <int MODE, int STAGES, int KSUB>
+struct DecCfg {
+  static constexpr int kTiles = MODE == kGateUp ? 2 : 1;  // weight tiles (accumulators) per unit
+  static constexpr int kWBytes = kTiles * 128 * BK;
+  static constexpr int kTBytes = kNt * BK;
+  static constexpr int kSubBytes = kWBytes + kTBytes;
+  static constexpr int kStageBytes = KSUB * kSubBytes;
+  static constexpr int kBufs = 4;
+  static constexpr int kBufCols = kTiles * kNt;
+  static constexpr int kTmem = kBufs * kBufCols;
+  static constexpr int kScaleBytes = 4 * 2 * kTiles * kNt * 4;  // warp x parity x tile x row
+  static constexpr int kStartBytes = (kMaxSegments + 1) * 4;
+  static constexpr int kMaxBytes = 2 * 4 * kNt * 4;  // gate_up: unit parity x warp x row
+  static constexpr int kPartBytes = MODE == kPlain ? 128 * kNt * 4 : 0;  // SPLIT's partial sums
+  static constexpr size_t kSmem = (size_t)STAGES * kStageBytes + 1024 + kBarBytes + kScaleBytes +
+                                  kMaxBytes + kPartBytes + kStartBytes;
+  static_assert(kTmem <= 512 && (kTmem & (kTmem - 1)) == 0, "TMEM columns");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void st_cluster_f32(const void* local, uint32_t rank, float v) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(r), "f"(v) : "memory");
+}
+
+template <int MODE, int STAGES, int KSUB, bool SPLIT>
+__global__ void __launch_bounds__(kDecThreads, 1)
+    k_gemm_fp8_dec(const __grid_constant__ CUtensorMap tmW0,
+                   const __grid_constant__ CUtensorMap tmW1,
+                   const __grid_constant__ CUtensorMap tmT, const __grid_constant__ Args a) {
+  using C = DecCfg<MODE, STAGES, KSUB>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* tail = smem + STAGES * C::kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(tail);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + C::kBufs;
+  uint64_t* hmax = tempty + C::kBufs;  // gate_up: the four warps' maxima are there
+  uint64_t* never = hmax + 1;
+  uint64_t* drain = never + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((2 * STAGES + 2 * C::kBufs + 3) * 8 + 8 <= kBarBytes, "barriers");
+  float* scale_x = reinterpret_cast<float*>(tail + kBarBytes);
+  uint32_t* max_x = reinterpret_cast<uint32_t*>(tail + kBarBytes + C::kScaleBytes);
+  float* part = reinterpret_cast<float*>(tail + kBarBytes + C::kScaleBytes + C::kMaxBytes);
+  int32_t* tile_start = reinterpret_cast<int32_t*>(tail + kBarBytes + C::kScaleBytes +
+                                                   C::kMaxBytes + C::kPartBytes);
+  __shared__ int32_t warp_tot[kDecThreads / 32];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int KB = (a.K + BK - 1) / BK;
+  const int NB = (a.N + 127) / 128;  // weight blocks = scale rows
+  const uint32_t csize = SPLIT ? cluster_size() : 1, crank = SPLIT ? cluster_rank() : 0;
+  const int64_t unit0 = blockIdx.x / csize, unit_step = gridDim.x / csize;
+  const int kb0 = (int)((int64_t)crank * KB / csize);
+  const int kb1 = (int)((int64_t)(crank + 1) * KB / csize);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < C::kBufs; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 4);
+    }
+    mbar_init(hmax, 4);
+    mbar_init(never, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    sm100::mbar_init_fence();
+  }
+  if (warp == 4 && lane == 0) {
+    prefetch_map(&tmW0);
+    prefetch_map(&tmT);
+    if (MODE == kGateUp) prefetch_map(&tmW1);
+  }
+  if (warp == 5) sm100::tmem_alloc(tmem_slot, C::kTmem);
+  if (!a.early) pdl_wait();
+  tc_fence_before();
+  build_tiles<kDecThreads>(a, kNt, tile_start, warp_tot);
+  tc_fence_after();
+  if (SPLIT) cluster_sync();  // the other CTAs run: their shared memory may be written
+  const uint32_t tmem_base = *tmem_slot;
+  const int64_t total_units = (int64_t)tile_start[a.E] * NB;
+  auto unit_of = [&](int64_t u) { return unit_at(a, tile_start, NB, kNt, u); };
+
+  if (warp == 4) {
+    // ------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint64_t wpol = sm100::l2_evict_first_policy();
+      int stage = 0;
+      uint32_t phase = 0;
+      int64_t filled = 0;  // stages handed to TMA so far
+      bool ok = true;
+      if (a.probe) ok = mbar_wait(never, 0, abort_flag, kProbeLimitNs);
+      bool dep_pending = a.early != 0;
+      for (int64_t u = unit0; u < total_units && ok; u += unit_step) {
+        const Unit w = unit_of(u);
+        const int nbox = (w.nrows + kSmallBox - 1) / kSmallBox;
+        const uint32_t bytes = C::kWBytes + nbox * kSmallBox * BK;  // of a K block
+        auto load_w = [&](int kb, int s) {
+          mbar_arrive_expect_tx(&full[s], bytes * (kb1 - kb < KSUB ? kb1 - kb : KSUB));
+#pragma unroll
+          for (int i = 0; i < C::kTiles; ++i)
+#pragma unroll
+            for (int j = 0; j < KSUB; ++j)
+              if (kb + j < kb1)
+                sm100::tma_load_3d_hint(i == 0 ? &tmW0 : &tmW1, &full[s],
+                                        smem + s * C::kStageBytes + j * C::kSubBytes +
+                                            i * 128 * BK,
+                                        (kb + j) * BK, w.nb * 128, w.e, wpol);
+        };
+        auto load_t = [&](int kb, int s) {
+#pragma unroll
+          for (int j = 0; j < KSUB; ++j)
+            if (kb + j < kb1)
+              for (int i = 0; i < nbox; ++i)
+                tma_load_2d(&tmT, &full[s],
+                            smem + s * C::kStageBytes + j * C::kSubBytes + C::kWBytes +
+                                i * kSmallBox * BK,
+                            (kb + j) * BK, w.row0 + i * kSmallBox);
+        };
+        int kb = kb0;
+        if (dep_pending) {
+          // the weights of up to STAGES stages first, then the wait for the
+          // kernel that writes the rows, then their rows
+          for (int j = 0; j < STAGES && kb < kb1; ++j, kb += KSUB) {
+            load_w(kb, stage);
+            ++filled;
+            if (++stage == STAGES) { stage = 0; phase ^= 1; }
+          }
+          pdl_wait();
+          dep_pending = false;
+          for (int j = 0; kb0 + j * KSUB < kb; ++j) load_t(kb0 + j * KSUB, j);
+        }
+        for (; kb < kb1; kb += KSUB) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
+          load_w(kb, stage);
+          load_t(kb, stage);
+          ++filled;
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        }
+      }
+      if (dep_pending) pdl_wait();
+      pdl_trigger();
+      if (!ok) {
+        record_error(a.st, MOE_ERR_DEVICE_TIMEOUT, 350 + MODE);
+        *abort_flag = 1;
+        volatile int go_on = 0;  // the CTA's copies in flight land before it ends
+        for (int64_t f = filled > STAGES ? filled - STAGES : 0; f < filled; ++f)
+          mbar_wait(&full[f % STAGES], (uint32_t)(f / STAGES) & 1, &go_on, kDrainNs);
+      }
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, tphase = 0;
+      bool ok = true;
+      const uint64_t desc0 = sm100::smem_desc(smem_u32(smem), 1024, 2);
+      for (int64_t u = unit0; u < total_units && ok; u += unit_step) {
+        const Unit w = unit_of(u);
+        const uint32_t idesc = idesc_e4m3(128, (w.nrows + 15) / 16 * 16);
+        for (int kb = kb0; kb < kb1 && ok; kb += KSUB) {
+          if (!mbar_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
+#pragma unroll
+          for (int j = 0; j < KSUB; ++j) {
+            if (kb + j >= kb1) break;
+            if (!mbar_wait(&tempty[buf], tphase ^ 1, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t dw =
+                desc0 + (uint64_t)(stage * (C::kStageBytes >> 4) + j * (C::kSubBytes >> 4));
+            const uint64_t dt = dw + (uint64_t)(C::kWBytes >> 4);
+            const uint32_t d = tmem_base + buf * C::kBufCols;
+#pragma unroll
+            for (int k = 0; k < BK / UK; ++k)
+#pragma unroll
+              for (int i = 0; i < C::kTiles; ++i)
+                umma_e4m3(d + i * kNt, dw + (uint64_t)((i * 128 * BK + k * UK) >> 4),
+                          dt + (uint64_t)(k * UK >> 4), idesc, k != 0);
+            umma_commit(&tfull[buf]);
+            if (++buf == C::kBufs) { buf = 0; tphase ^= 1; }
+          }
+          if (ok) umma_commit(&empty[stage]);
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        }
+      }
+      if (!ok) {
+        record_error(a.st, MOE_ERR_DEVICE_TIMEOUT, 360 + MODE);
+        *abort_flag = 1;
+        volatile int go_on = 0;
+        umma_commit(drain);
+        mbar_wait(drain, 0, &go_on, kDrainNs);
+      }
+    }
+  } else {
+    // ------------------------------------------------------ epilogue
+    const bool has_lb = !(a.lbeta == 0.0f || a.lbeta != a.lbeta);
+    const float b_eff = (a.beta == 0.0f || a.beta != a.beta) ? 1.0f : a.beta;
+    const uint32_t lanes0 = tmem_base + ((uint32_t)(warp * 32) << 16);
+    float* sc = scale_x + warp * 2 * C::kTiles * kNt;
+    if (a.early) pdl_wait();
+    int buf = 0;
+    uint32_t tphase = 0, parity = 0;
+    bool ok = true;
+    for (int64_t u = unit0; u < total_units && ok; u += unit_step) {
+      const Unit w = unit_of(u);
+      // lane t fetches the scales of token row t, kAhead blocks before their use
+      const float* sxp =
+          a.xs + ((int64_t)w.row0 + (lane < w.nrows ? lane : w.nrows - 1)) * KB;
+      const float* w0p = a.ws0 + ((int64_t)w.e * NB + w.nb) * KB;
+      const float* w1p = MODE == kGateUp ? a.ws1 + ((int64_t)w.e * NB + w.nb) * KB : nullptr;
+      uint64_t acc2[C::kTiles][kNt / 2];  // the sums of token rows 2i and 2i + 1
+#pragma unroll
+      for (int t = 0; t < C::kTiles; ++t)
+#pragma unroll
+        for (int i = 0; i < kNt / 2; ++i) acc2[t][i] = 0;
+      constexpr int kAhead = 4;
+      float sxr[kAhead], w0r[kAhead], w1r[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int b = kb0 + j < KB ? kb0 + j : KB - 1;
+        sxr[j] = __ldg(sxp + b);
+        w0r[j] = __ldg(w0p + b);
+        w1r[j] = MODE == kGateUp ? __ldg(w1p + b) : 0.0f;
+      }
+      for (int kb = kb0; kb < kb1; ++kb) {
+        float* scp = sc + (kb & 1) * C::kTiles * kNt;
+        scp[lane] = sxr[0] * w0r[0];
+        if (MODE == kGateUp) scp[kNt + lane] = sxr[0] * w1r[0];
+#pragma unroll
+        for (int j = 0; j + 1 < kAhead; ++j) {
+          sxr[j] = sxr[j + 1];
+          w0r[j] = w0r[j + 1];
+          w1r[j] = w1r[j + 1];
+        }
+        const int b = kb + kAhead < KB ? kb + kAhead : KB - 1;
+        sxr[kAhead - 1] = __ldg(sxp + b);
+        w0r[kAhead - 1] = __ldg(w0p + b);
+        if (MODE == kGateUp) w1r[kAhead - 1] = __ldg(w1p + b);
+        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[buf], tphase, abort_flag))) {
+          if (lane == 0) record_error(a.st, MOE_ERR_DEVICE_TIMEOUT, 370 + MODE);
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        __syncwarp();  // the products sx * sw are in shared memory
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kNt; c += 16) {
+          if (c < w.nrows) {
+#pragma unroll
+            for (int t = 0; t < C::kTiles; ++t) {
+              uint32_t r[16];
+              sm100::tmem_ld16(lanes0 + buf * C::kBufCols + t * kNt + c, r);
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                const ulonglong2 f =
+                    *reinterpret_cast<const ulonglong2*>(scp + t * kNt + c + i);
+                fma2(acc2[t][(c + i) / 2], r[i], r[i + 1], f.x);
+                fma2(acc2[t][(c + i) / 2 + 1], r[i + 2], r[i + 3], f.y);
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[buf]);
+        if (++buf == C::kBufs) { buf = 0; tphase ^= 1; }
+      }
+      if (!ok) break;
+      const int m = 32 * warp + lane;  // this thread's row of the weight block
+      const int n = w.nb * 128 + m;
+      float acc[C::kTiles][kNt];
+#pragma unroll
+      for (int t = 0; t < C::kTiles; ++t)
+#pragma unroll
+        for (int i = 0; i < kNt / 2; ++i) {
+          acc[t][2 * i] = lo_of(acc2[t][i]);
+          acc[t][2 * i + 1] = hi_of(acc2[t][i]);
+        }
+      if (MODE == kPlain && SPLIT) {
+        // weight row m is finished by CTA m / rpc of the cluster
+        const int rpc = 128 / csize;
+#pragma unroll
+        for (int i = 0; i < kNt; ++i)
+          if (i < w.nrows)
+            st_cluster_f32(part + ((int)crank * kNt + i) * rpc + m % rpc, m / rpc, acc[0][i]);
+      } else if (MODE == kPlain) {
+        if (n < a.N) {
+          const int64_t at = (int64_t)w.row0 * a.N + n;
+#pragma unroll
+          for (int i = 0; i < kNt; ++i)
+            if (i < w.nrows) {
+              float v = acc[0][i];
+              if (a.res) v += __bfloat162float(a.res[at + (int64_t)i * a.N]);
+              a.y[at + (int64_t)i * a.N] = __float2bfloat16_rn(v);
+            }
+        }
+      } else {
+        // h of one d_ff row and all token rows; the largest |h| of a token row
+        // over the 128 d_ff rows: over the warp, then over the four warps
+        // through shared memory (two buffers, so a fast warp's next unit cannot
+        // overwrite what a slow one still reads)
+        uint32_t mine = 0;  // lane i: the warp's largest magnitude of token row i
+        uint32_t* mx = max_x + parity * 4 * kNt;
+#pragma unroll
+        for (int i = 0; i < kNt; ++i) {
+          if (i < w.nrows) {
+            acc[0][i] = act32(acc[0][i], acc[C::kTiles - 1][i], a.act_kind, b_eff, a.lbeta, has_lb);
+            const uint32_t v =
+                __reduce_max_sync(0xffffffffu, __float_as_uint(acc[0][i]) & 0x7fffffffu);
+            if (lane == i) mine = v;
+          }
+        }
+        mx[warp * kNt + lane] = mine;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(hmax);
+        if (!__all_sync(0xffffffffu, mbar_wait(hmax, parity, abort_flag))) {
+          if (lane == 0) record_error(a.st, MOE_ERR_DEVICE_TIMEOUT, 380);
+          *abort_flag = 1;
+          break;
+        }
+        mine = max(max(mx[lane], mx[kNt + lane]), max(mx[2 * kNt + lane], mx[3 * kNt + lane]));
+        parity ^= 1;
+        float inv;
+        const float s = fp8::block_scale(__uint_as_float(mine), a.pow2, inv);
+        if (warp == 0 && lane < w.nrows) a.hs[((int64_t)w.row0 + lane) * NB + w.nb] = s;
+        uint8_t* dst = a.hq + (int64_t)w.row0 * a.N + n;
+#pragma unroll
+        for (int i = 0; i < kNt; i += 2) {
+          if (i < w.nrows) {
+            const float q0 = acc[0][i] * __shfl_sync(0xffffffffu, inv, i);
+            const float q1 = acc[0][i + 1] * __shfl_sync(0xffffffffu, inv, i + 1);
+            const uint32_t q = fp8::pack4(q0, q1, 0.0f, 0.0f);
+            if (n < a.N) {
+              dst[(int64_t)i * a.N] = (uint8_t)q;
+              if (i + 1 < w.nrows) dst[(int64_t)(i + 1) * a.N] = (uint8_t)(q >> 8);
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (SPLIT) {
+    cluster_sync();  // every CTA's part of this CTA's rows has arrived
+    if (unit0 < total_units && !*abort_flag) {
+      const Unit w = unit_of(unit0);
+      const int rpc = 128 / csize;
+      for (int i = threadIdx.x; i < rpc * w.nrows; i += kDecThreads) {
+        const int t = i / rpc, m = i - t * rpc;
+        const int n = w.nb * 128 + (int)crank * rpc + m;
+        float v = part[t * rpc + m];
+        for (int r = 1; r < (int)csize; ++r) v += part[(r * kNt + t) * rpc + m];
+        if (n < a.N) {
+          const int64_t at = ((int64_t)w.row0 + t) * a.N + n;
+          if (a.res) v += __bfloat162float(a.res[at]);
+          a.y[at] = __float2bfloat16_rn(v);
+        }
+      }
+    }
+  }
+  if (warp == 5) {
+    __syncwarp();
+    tc_fence_after();
+    sm100::tmem_dealloc(tmem_base, C::kTmem);
   }
 }
 
@@ -584,11 +1013,17 @@ bool map_rows(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, ui
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, int BN, int TM, int STAGES>
+// Token tiles that S rows in E segments can need at most.
+int64_t max_tiles(const Args& a, int tile) {
+  if (!a.offsets) return (a.S + tile - 1) / tile;
+  return a.S / tile + (a.S < a.E ? a.S : a.E);
+}
+
+template <int MODE, int BN, int STAGES>
 cudaError_t launch(const CUtensorMap& b0, const CUtensorMap& b1, const CUtensorMap& a16,
                    const CUtensorMap& a128, const Args& args, cudaStream_t s) {
-  using C = Cfg<MODE, BN, TM, STAGES>;
-  constexpr auto kernel = k_gemm_fp8<MODE, BN, TM, STAGES>;
+  using C = Cfg<MODE, BN, STAGES>;
+  constexpr auto kernel = k_gemm_fp8<MODE, BN, STAGES>;
   static std::once_flag once[kMaxDevices];
   static cudaError_t set_up[kMaxDevices];
   const cudaError_t e = once_per_device(once, set_up, [&](int) {
@@ -596,34 +1031,115 @@ cudaError_t launch(const CUtensorMap& b0, const CUtensorMap& b1, const CUtensorM
                                 (int)C::kSmem);
   });
   if (e != cudaSuccess) return e;
-  // no more CTAs than units: at most one token tile per TM rows and segment
   const int cols = MODE == kGateUp ? 128 : BN;
-  const int64_t tiles = args.S / TM + (args.S < args.E ? args.S : args.E);
-  const int64_t units = tiles * ((args.N + cols - 1) / cols);
+  const int64_t units = max_tiles(args, BM) * ((args.N + cols - 1) / cols);
   const int sms = dev_info()->sm_count;
   return launch_pdl(kernel, dim3((unsigned)(units < sms ? units : sms)), dim3(kThreads), C::kSmem,
                     s, b0, b1, a16, a128, args);
 }
 
+template <int MODE, int STAGES, int KSUB, bool SPLIT>
+cudaError_t launch_dec(const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& t,
+                       const Args& args, unsigned grid, unsigned cluster, cudaStream_t s) {
+  using C = DecCfg<MODE, STAGES, KSUB>;
+  constexpr auto kernel = k_gemm_fp8_dec<MODE, STAGES, KSUB, SPLIT>;
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t set_up[kMaxDevices];
+  const cudaError_t e = once_per_device(once, set_up, [&](int) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)C::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kDecThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = SPLIT ? 2 : 1;
+  return counted(cudaLaunchKernelEx(&cfg, kernel, w0, w1, t, args));
+}
+
+// How many clusters of the split decode kernel, of 2, 4 and 8 CTAs, can run at once.
+int max_clusters(unsigned c) {
+  constexpr int kLog = 4;
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t set_up[kMaxDevices];
+  static int most[kMaxDevices][kLog];
+  using C = DecCfg<kPlain, 5, 2>;
+  constexpr auto kernel = k_gemm_fp8_dec<kPlain, 5, 2, true>;
+  const cudaError_t e = once_per_device(once, set_up, [&](int dev) {
+    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)C::kSmem);
+    for (int i = 1; i < kLog && r == cudaSuccess; ++i) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 1u << i;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3((unsigned)(dev_info()->sm_count >> i) << i);
+      cfg.blockDim = dim3(kDecThreads);
+      cfg.dynamicSmemBytes = C::kSmem;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      r = cudaOccupancyMaxActiveClusters(&most[dev][i], kernel, &cfg);
+    }
+    return r;
+  });
+  int dev = 0;
+  if (e != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return most[dev][c == 8 ? 3 : c == 4 ? 2 : 1];
+}
+
+struct Operands {
+  const uint8_t* xq;
+  const uint8_t* w0;
+  const uint8_t* w1;  // gate_up
+};
+
 template <int MODE>
-cudaError_t launch_variant(const CUtensorMap& b0, const CUtensorMap& b1, const CUtensorMap& a16,
-                           const CUtensorMap& a128, const Args& args, cudaStream_t s) {
+int run_product(const Operands& o, const Args& args, cudaStream_t s) {
+  const int sms = dev_info()->sm_count;
+  CUtensorMap w0, w1, t, t128;
+  if (!map_weights(&w0, o.w0, args.K, args.N, args.E) ||
+      !map_rows(&t, o.xq, args.K, args.S, kSmallBox))
+    return MOE_ERR_CUDA;
+  if (MODE == kGateUp && !map_weights(&w1, o.w1, args.K, args.N, args.E)) return MOE_ERR_CUDA;
+  cudaError_t e;
   if (args.S <= 16 * (int64_t)args.E) {
-    if constexpr (MODE == kGateUp) return launch<MODE, 256, 32, 6>(b0, b1, a16, a128, args, s);
-    else return launch<MODE, 128, 32, 10>(b0, b1, a16, a128, args, s);
+    const int64_t units = max_tiles(args, kNt) * ((args.N + 127) / 128);
+    const unsigned grid = (unsigned)(units < sms ? units : sms);
+    if constexpr (MODE == kGateUp) {
+      e = launch_dec<MODE, 3, 2, false>(w0, w1, t, args, grid, 1, s);
+    } else {
+      // a unit's K shared by a cluster while that fills more SMs, every cluster
+      // can run at once and each CTA keeps at least two K blocks
+      const int KB = (args.K + BK - 1) / BK;
+      unsigned c = 1;
+      while (c < 8 && units * c * 2 <= sms && KB >= 4 * (int)c && units <= max_clusters(2 * c))
+        c *= 2;
+      e = c > 1 ? launch_dec<MODE, 5, 2, true>(w0, w0, t, args, (unsigned)units * c, c, s)
+                : launch_dec<MODE, 5, 2, false>(w0, w0, t, args, grid, 1, s);
+    }
+  } else {
+    if (!map_rows(&t128, o.xq, args.K, args.S, BM)) return MOE_ERR_CUDA;
+    e = launch<MODE, 256, 4>(w0, MODE == kGateUp ? w1 : w0, t, t128, args, s);
   }
-  return launch<MODE, 256, 128, 4>(b0, b1, a16, a128, args, s);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
 
 int grouped_fp8_run(const uint8_t* xq, const float* xs, const int32_t* offsets, int E, int64_t S,
                     int K, const uint8_t* w, const float* ws, int N, const __nv_bfloat16* residual,
-                    __nv_bfloat16* y, DeviceStatus* st, cudaStream_t s, bool early) {
-  CUtensorMap mw, m16, m128;
-  if (!map_weights(&mw, w, K, N, E) || !map_rows(&m16, xq, K, S, kSmallBox) ||
-      !map_rows(&m128, xq, K, S, 128))
-    return MOE_ERR_CUDA;
+                    __nv_bfloat16* y, DeviceStatus* st, cudaStream_t s, bool early, bool reset) {
   Args a{};
   a.offsets = offsets;
   a.E = E;
@@ -635,9 +1151,10 @@ int grouped_fp8_run(const uint8_t* xq, const float* xs, const int32_t* offsets, 
   a.y = y;
   a.res = residual;
   a.early = early ? 1 : 0;
+  a.reset = reset ? 1 : 0;
   a.probe = wait_probe();
   a.st = st;
-  return launch_variant<kPlain>(mw, mw, m16, m128, a, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return run_product<kPlain>({xq, w, nullptr}, a, s);
 }
 
 size_t expert_fp8_scratch_bytes(int64_t S, int F) {
@@ -649,13 +1166,9 @@ int expert_ffn_fp8_run(const uint8_t* xq, const float* xs, const int32_t* offset
                        int d, int F, const uint8_t* w1, const float* w1s, const uint8_t* w3,
                        const float* w3s, const uint8_t* w2, const float* w2s,
                        const moe_act_cfg& act, bool pow2, __nv_bfloat16* y, void* scratch,
-                       DeviceStatus* st, cudaStream_t s) {
+                       DeviceStatus* st, cudaStream_t s, bool reset) {
   uint8_t* hq = static_cast<uint8_t*>(scratch);
   float* hs = reinterpret_cast<float*>(hq + align_up((size_t)S * (size_t)F, 256));
-  CUtensorMap mw1, mw3, m16, m128;
-  if (!map_weights(&mw1, w1, d, F, E) || !map_weights(&mw3, w3, d, F, E) ||
-      !map_rows(&m16, xq, d, S, kSmallBox) || !map_rows(&m128, xq, d, S, 128))
-    return MOE_ERR_CUDA;
   Args a{};
   a.offsets = offsets;
   a.E = E;
@@ -671,12 +1184,14 @@ int expert_ffn_fp8_run(const uint8_t* xq, const float* xs, const int32_t* offset
   a.beta = act.beta;
   a.lbeta = act.linear_beta;
   a.pow2 = pow2 ? 1 : 0;
+  a.reset = reset ? 1 : 0;
   a.probe = wait_probe();
   a.st = st;
-  if (launch_variant<kGateUp>(mw1, mw3, m16, m128, a, s) != cudaSuccess) return MOE_ERR_CUDA;
+  const int rc = run_product<kGateUp>({xq, w1, w3}, a, s);
+  if (rc) return rc;
   // offsets were read by the kernel just launched, after its own wait: the
   // down kernel may read them, and fetch weights, before that kernel ends
-  return grouped_fp8_run(hq, hs, offsets, E, S, F, w2, w2s, d, nullptr, y, st, s, true);
+  return grouped_fp8_run(hq, hs, offsets, E, S, F, w2, w2s, d, nullptr, y, st, s, true, false);
 }
 
 }  // namespace moe

@@ -214,16 +214,17 @@ cudaError_t launch_quantize_blocks(const __nv_bfloat16* x, int64_t B, int64_t M,
 // gemm_fp8.cu: products of 8-bit block-scaled operands.
 // offsets [E + 1], or nullptr with E = 1: one segment of all S rows.
 // early: offsets were complete before the kernel preceding on `s` started.
+// reset: the (first) kernel clears the status word, as reset_status would.
 int grouped_fp8_run(const uint8_t* xq, const float* xs, const int32_t* offsets, int E, int64_t S,
                     int K, const uint8_t* w, const float* ws, int N, const __nv_bfloat16* residual,
-                    __nv_bfloat16* y, DeviceStatus* st, cudaStream_t s, bool early);
+                    __nv_bfloat16* y, DeviceStatus* st, cudaStream_t s, bool early, bool reset);
 // h [S, F] e4m3 and its scales [S, ceil(F / 128)]
 size_t expert_fp8_scratch_bytes(int64_t S, int F);
 int expert_ffn_fp8_run(const uint8_t* xq, const float* xs, const int32_t* offsets, int E, int64_t S,
                        int d, int F, const uint8_t* w1, const float* w1s, const uint8_t* w3,
                        const float* w3s, const uint8_t* w2, const float* w2s,
                        const moe_act_cfg& act, bool pow2, __nv_bfloat16* y, void* scratch,
-                       DeviceStatus* st, cudaStream_t s);
+                       DeviceStatus* st, cudaStream_t s, bool reset);
 
 // The diagnostics hook's switch (moe_set_wait_probe), read at every launch,
 // and the limit of the wait that it makes run out.
