@@ -12,6 +12,7 @@ binding's functions raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -684,10 +685,37 @@ def _fp8_call(fn: str, dev: int, *args):
 def _ws_for(ws, need, dev):
     if ws is None:
         torch = _torch()
-        return torch.empty(need, dtype=torch.uint8, device=dev)
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
     if ws.get_device() != dev:
         raise ValueError(f"ws is on {ws.device}, expected cuda:{dev}")
     return ws
+
+
+_status_only = {}  # device index -> 256 bytes
+
+
+def _status_ws(ws, dev):
+    """The workspace of a call that needs only the status word: the caller's, or
+    one that the calls of a device share (nothing reads its status)."""
+    if ws is not None:
+        return _ws_for(ws, 0, dev)
+    w = _status_only.get(dev)
+    if w is None:
+        torch = _torch()
+        w = torch.empty(256, dtype=torch.uint8, device=dev)
+        if not torch.cuda.is_current_stream_capturing():  # not memory of a graph's pool
+            _status_only[dev] = w
+    return w
+
+
+@functools.lru_cache(maxsize=256)
+def _dispatch_ws(N, K, E):
+    return lib().moe_dispatch_workspace_size(N, K, E)
+
+
+@functools.lru_cache(maxsize=256)
+def _ffn_fp8_ws(S, d, E, F):
+    return lib().moe_expert_ffn_fp8_workspace_size(S, d, E, F)
 
 
 def _opt(t):
@@ -725,8 +753,8 @@ def quantize_fp8(x, block_rows: int = 1, pow2_scales: bool = False, q=None, scal
     if scale is not None:
         named.append(("scale", scale, torch.float32, s_shape))
     dev = _fp8_args(*named)
-    q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev) if q is None else q
-    scale = torch.empty(s_shape, dtype=torch.float32, device=dev) if scale is None else scale
+    q = torch.empty_like(x, dtype=torch.float8_e4m3fn) if q is None else q
+    scale = x.new_empty(s_shape, dtype=torch.float32) if scale is None else scale
     _fp8_call("moe_quantize_fp8", dev, x.data_ptr(), B, M, K, block_rows, int(pow2_scales),
               q.data_ptr(), scale.data_ptr())
     return q, scale
@@ -742,17 +770,18 @@ def dispatch_fp8(topk_idx, x_e, num_experts: int, pow2_scales: bool = False, ws=
     E, S = num_experts, N * K
     dev = _fp8_args(("x_e", x_e, torch.bfloat16, (N, d_e)),
                     ("topk_idx", topk_idx, torch.int32, None))
-    i32 = torch.int32
-    counts = torch.empty(E, dtype=i32, device=dev)
-    offsets = torch.empty(E + 1, dtype=i32, device=dev)
-    perm = torch.empty(S, dtype=i32, device=dev)
-    pos = torch.empty(S, dtype=i32, device=dev)
-    xq = torch.empty((S, d_e), dtype=torch.float8_e4m3fn, device=dev)
-    xs = torch.empty((S, _c128(d_e)), dtype=torch.float32, device=dev)
-    ws = _ws_for(ws, lib().moe_dispatch_workspace_size(N, K, E), dev)
+    need = _dispatch_ws(N, K, E)
+    # one allocation for the integers and, at its start, the workspace
+    at = 0 if ws is not None else (need + 255) // 256 * 64
+    ints = x_e.new_empty(at + 2 * E + 1 + 2 * S, dtype=torch.int32)
+    own_ws, counts, offsets, perm, pos = ints.split((at, E, E + 1, S, S))
+    xq = x_e.new_empty((S, d_e), dtype=torch.float8_e4m3fn)
+    xs = x_e.new_empty((S, _c128(d_e)), dtype=torch.float32)
+    ws_p, ws_n = ((own_ws.data_ptr(), 4 * at) if ws is None else
+                  (_ws_for(ws, 0, dev).data_ptr(), ws.numel()))
     _fp8_call("moe_dispatch_fp8", dev, topk_idx.data_ptr(), N, K, E, x_e.data_ptr(), d_e,
               int(pow2_scales), counts.data_ptr(), offsets.data_ptr(), perm.data_ptr(),
-              pos.data_ptr(), xq.data_ptr(), xs.data_ptr(), ws.data_ptr(), ws.numel())
+              pos.data_ptr(), xq.data_ptr(), xs.data_ptr(), ws_p, ws_n)
     return counts, offsets, perm, pos, xq, xs
 
 
@@ -771,8 +800,8 @@ def linear_fp8(xq, x_scale, w, w_scale, residual=None, out=None, ws=None):
     if out is not None:
         named.append(("out", out, bf, (M, N)))
     dev = _fp8_args(*named)
-    ws = _ws_for(ws, 256, dev)  # moe_linear_fp8_workspace_size: the status word
-    out = torch.empty((M, N), dtype=bf, device=dev) if out is None else out
+    ws = _status_ws(ws, dev)  # moe_linear_fp8_workspace_size: the status word
+    out = xq.new_empty((M, N), dtype=bf) if out is None else out
     _fp8_call("moe_linear_fp8", dev, xq.data_ptr(), x_scale.data_ptr(), M, K, w.data_ptr(),
               w_scale.data_ptr(), N, _opt(residual), out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
@@ -793,8 +822,8 @@ def grouped_linear_fp8(xq, x_scale, offsets, w, w_scale, out=None, ws=None):
     if out is not None:
         named.append(("out", out, bf, (S, N)))
     dev = _fp8_args(*named)
-    ws = _ws_for(ws, 256, dev)  # moe_grouped_linear_fp8_workspace_size: the status word
-    out = torch.empty((S, N), dtype=bf, device=dev) if out is None else out
+    ws = _status_ws(ws, dev)  # moe_grouped_linear_fp8_workspace_size: the status word
+    out = xq.new_empty((S, N), dtype=bf) if out is None else out
     _fp8_call("moe_grouped_linear_fp8", dev, xq.data_ptr(), x_scale.data_ptr(),
               offsets.data_ptr(), E, S, K, w.data_ptr(), w_scale.data_ptr(), N, out.data_ptr(),
               ws.data_ptr(), ws.numel())
@@ -828,11 +857,11 @@ def expert_ffn_fp8(xq, x_scale, offsets, w1, w1_scale, w3, w3_scale, w2, w2_scal
     if y is not None:
         named.append(("y", y, torch.bfloat16, (S, d)))
     dev = _fp8_args(*named)
-    need = lib().moe_expert_ffn_fp8_workspace_size(S, d, E, F)
+    need = _ffn_fp8_ws(S, d, E, F)
     if need == 0:
         raise MoeError("moe_expert_ffn_fp8_workspace_size", -2)
     ws = _ws_for(ws, need, dev)
-    y = torch.empty((S, d), dtype=torch.bfloat16, device=dev) if y is None else y
+    y = xq.new_empty((S, d), dtype=torch.bfloat16) if y is None else y
     a = act._c()
     _fp8_call("moe_expert_ffn_fp8", dev, xq.data_ptr(), x_scale.data_ptr(), offsets.data_ptr(), E,
               S, d, F, ctypes.byref(xw), ctypes.byref(a), int(pow2_scales), y.data_ptr(),

@@ -679,8 +679,8 @@ int moe_dispatch_fp8(const int32_t* topk_idx, int64_t N, int K, int E, const moe
   if ((rc = check_ws(ws, ws_bytes, moe_dispatch_workspace_size(N, K, E)))) return rc;
   if ((rc = check_device())) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((rc = reset_status(ws, s))) return rc;
   if (N == 0) {
+    if ((rc = reset_status(ws, s))) return rc;
     if (cudaMemsetAsync(counts, 0, sizeof(int32_t) * E, s) != cudaSuccess ||
         cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (E + 1), s) != cudaSuccess)
       return MOE_ERR_CUDA;
@@ -688,7 +688,8 @@ int moe_dispatch_fp8(const int32_t* topk_idx, int64_t N, int K, int E, const moe
   }
   const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(x_e);
   if (launch_dispatch(topk_idx, N, K, E, x, d_e, counts, offsets, perm, pos, nullptr,
-                      reinterpret_cast<int32_t*>(body_of(ws)), status_of(ws), s) != cudaSuccess ||
+                      reinterpret_cast<int32_t*>(body_of(ws)), status_of(ws), s,
+                      true) != cudaSuccess ||
       launch_quantize_rows(x, N, d_e, pow2_scales != 0, xq, x_scale, pos, K, N * K, s) !=
           cudaSuccess)
     return MOE_ERR_CUDA;

@@ -223,9 +223,13 @@ __global__ void __launch_bounds__(1024) k_sort_small(const int32_t* __restrict__
                                                      int32_t* __restrict__ offsets,
                                                      int32_t* __restrict__ perm,
                                                      int32_t* __restrict__ pos,
-                                                     DeviceStatus* st) {
+                                                     DeviceStatus* st, int reset) {
   pdl_wait();
   pdl_trigger();
+  if (reset) {  // the first kernel of its call clears the status word
+    if (threadIdx.x == 0) *st = DeviceStatus{0, 0};
+    __syncthreads();
+  }
   extern __shared__ int16_t cnt_raw[];  // [32][E]
   __shared__ int32_t warp_tot[32];
   auto cnt = [&](int w, int e) -> int16_t& { return cnt_raw[w * E + e]; };
@@ -418,7 +422,7 @@ size_t dispatch_scratch_bytes(int64_t S, int E) {
 cudaError_t launch_dispatch(const int32_t* idx, int64_t N, int K, int E, const __nv_bfloat16* x_e,
                             int d_e, int32_t* counts, int32_t* offsets, int32_t* perm,
                             int32_t* pos, __nv_bfloat16* xs, int32_t* scratch, DeviceStatus* st,
-                            cudaStream_t s) {
+                            cudaStream_t s, bool reset) {
   const int64_t S = N * K;
   cudaError_t e;
   if (S >= 1 && S <= kSmallSortMaxS && E <= kSmallSortMaxE) {
@@ -431,9 +435,10 @@ cudaError_t launch_dispatch(const int32_t* idx, int64_t N, int K, int E, const _
       return e;
     const size_t smem = sizeof(int16_t) * 32 * (size_t)E;
     if ((e = launch_pdl(k_sort_small, dim3(1), dim3(1024), smem, s, idx, (int)S, E, counts,
-                        offsets, perm, pos, st)) != cudaSuccess)
+                        offsets, perm, pos, st, reset ? 1 : 0)) != cudaSuccess)
       return e;
   } else {
+    if (reset && (e = cudaMemsetAsync(st, 0, sizeof(DeviceStatus), s)) != cudaSuccess) return e;
     const int CH = dispatch_chunk_len(S);
     const int nchunks = dispatch_chunks(S);
     const size_t smem = sizeof(int32_t) * (size_t)E * kWarps;

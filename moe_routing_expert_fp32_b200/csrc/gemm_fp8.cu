@@ -61,16 +61,23 @@ constexpr uint64_t kDrainNs = 100000000ull;
 
 enum Mode { kPlain = 0, kGateUp = 1 };
 
-template <int MODE, int BN, int STAGES>
+// BN weight rows per unit: 256 keep the tensor cores busiest (a K block's tokens
+// are read from L2 once for twice the MMAs); 128 make twice the units, for
+// products whose units would not fill the GPU.  gate_up: 128 rows of w1 and the
+// same 128 of w3.
+template <int MODE, int BN>
 struct Cfg {
+  static constexpr int kStages = BN == 256 ? 4 : 6;
   static constexpr int kABytes = BM * BK;
   static constexpr int kBBytes = BN * BK;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kBufs = kTmemCols / BN;
   static constexpr int kStartBytes = (kMaxSegments + 1) * 4;
   static constexpr int kAmaxBytes = 2 * 2 * BM * 4;  // unit parity x half x row
-  static constexpr size_t kSmem = (size_t)STAGES * kStageBytes + 1024 + kBarBytes +
-                                  kAmaxBytes + kStartBytes;
+  static constexpr int kOutCols = 32;  // columns that a warp stores at a time
+  static constexpr int kOutBytes = 32 * kOutCols * 2;  // of a warp's 32 rows
+  static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024 + kBarBytes +
+                                  kAmaxBytes + kEpiWarps * kOutBytes + kStartBytes;
   static_assert(kABytes % 1024 == 0 && kBBytes % 1024 == 0, "1024-byte aligned operands");
   static_assert(MODE == kPlain || BN == 256, "gate_up: 128 rows of w1 and of w3");
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -129,27 +136,44 @@ __device__ __forceinline__ uint64_t pair_of(float v) {
 __device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
-// tanh in fp32 to about 1e-6: its Taylor series below 0.25 (where 1 - 2/(e^2x + 1)
-// would cancel), that form above.
-__device__ __forceinline__ float tanh32(float x) {
+// The activation in fp32, to about 2^-20 of its value.  sigmoid(g) = 1/(1 + e^-g);
+// tanh(x) = (e^2x - 1)/(e^2x + 1), the argument held below 10 where fp32's tanh is
+// 1, and below 0.25, where the numerator would cancel, its Taylor series.  The two
+// tanh share one reciprocal (the units that e^x and 1/x run on set the pace).
+struct Act {
+  bool situ, has_lb;
+  float beta, lbeta, inv_beta, inv_lbeta;
+};
+__device__ __forceinline__ Act make_act(int kind, float beta, float lbeta) {
+  Act t;
+  t.situ = kind == MOE_ACT_SITU;
+  t.has_lb = !(lbeta == 0.0f || lbeta != lbeta);
+  t.beta = (beta == 0.0f || beta != beta) ? 1.0f : beta;
+  t.lbeta = lbeta;
+  t.inv_beta = __fdiv_rn(1.0f, t.beta);
+  t.inv_lbeta = t.has_lb ? __fdiv_rn(1.0f, lbeta) : 0.0f;
+  return t;
+}
+// tanh(x) = num / den, den >= 1
+__device__ __forceinline__ void tanh_parts(float x, float& num, float& den) {
   const float x2 = x * x;
   const float p =
       x * (1.0f + x2 * (-1.0f / 3 + x2 * (2.0f / 15 + x2 * (-17.0f / 315 + x2 * (62.0f / 2835)))));
-  const float e = __expf(2.0f * fabsf(x));
-  const float t = copysignf(1.0f - __fdividef(2.0f, e + 1.0f), x);
-  return fabsf(x) < 0.25f ? p : t;
+  const float m = fabsf(x) > 10.0f ? 10.0f : fabsf(x);  // a NaN stays
+  const float e = __expf(2.0f * m);
+  const bool small = x2 < 0.0625f;
+  num = small ? p : copysignf(e - 1.0f, x);
+  den = small ? 1.0f : e + 1.0f;
 }
-__device__ __forceinline__ float sigmoid32(float x) {
-  return __fdividef(1.0f, 1.0f + __expf(-x));
-}
-__device__ __forceinline__ float act32(float g, float u, int kind, float beta, float lbeta,
-                                       bool has_lb) {
-  if (kind == MOE_ACT_SITU) {
-    const float t = beta * tanh32(__fdividef(g, beta));
-    const float up = has_lb ? lbeta * tanh32(__fdividef(u, lbeta)) : u;
-    return t * sigmoid32(g) * up;
-  }
-  return g * sigmoid32(g) * u;
+__device__ __forceinline__ float act32(float g, float u, const Act& t) {
+  const float sig = __fdividef(1.0f, 1.0f + __expf(-g));
+  if (!t.situ) return g * sig * u;
+  float n1, d1;
+  tanh_parts(g * t.inv_beta, n1, d1);
+  if (!t.has_lb) return t.beta * __fdividef(n1, d1) * sig * u;
+  float n2, d2;
+  tanh_parts(u * t.inv_lbeta, n2, d2);
+  return t.beta * t.lbeta * __fdividef(n1 * n2, d1 * d2) * sig;
 }
 
 // Token tiles of `tile` rows per segment and their prefix into tile_start
@@ -200,6 +224,26 @@ __device__ __forceinline__ void build_tiles(const Args& a, int tile, int32_t* ti
   __syncthreads();
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void st_cluster_f32(const void* local, uint32_t rank, float v) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(r), "f"(v) : "memory");
+}
+
 struct Unit {
   int e, row0, nrows, nb;
 };
@@ -222,12 +266,13 @@ __device__ __forceinline__ Unit unit_at(const Args& a, const int32_t* tile_start
   return r;
 }
 
-template <int MODE, int BN, int STAGES>
+template <int MODE, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     k_gemm_fp8(const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
                const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA128,
                const __grid_constant__ Args a) {
-  using C = Cfg<MODE, BN, STAGES>;
+  using C = Cfg<MODE, BN>;
+  constexpr int STAGES = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -242,7 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* amax_x = reinterpret_cast<float*>(tail + kBarBytes);
-  int32_t* tile_start = reinterpret_cast<int32_t*>(tail + kBarBytes + C::kAmaxBytes);
+  uint8_t* out_x = tail + kBarBytes + C::kAmaxBytes;
+  int32_t* tile_start = reinterpret_cast<int32_t*>(out_x + kEpiWarps * C::kOutBytes);
   static_assert((2 * STAGES + 2 * C::kBufs + 6) * 8 + 8 <= kBarBytes, "barriers");
   __shared__ int32_t warp_tot[kThreads / 32];
 
@@ -298,29 +344,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool dep_pending = a.early != 0;
       for (int64_t u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
         const Unit w = unit_of(u);
+        // token rows: one box of 128, or 16-row boxes for a short tile
         const bool big = w.nrows > 2 * kSmallBox;
-        const int nbox = big ? 1 : (w.nrows + kSmallBox - 1) / kSmallBox;
-        const uint32_t bytes = C::kBBytes + (big ? BM : nbox * kSmallBox) * BK;
+        const int box = big ? BM : kSmallBox;
+        const int nbox = (w.nrows + box - 1) / box;
+        const uint32_t bytes = C::kBBytes + nbox * box * BK;
         auto load_b = [&](int kb, int s) {
+          mbar_arrive_expect_tx(&full[s], bytes);
           uint8_t* sB = smem + s * C::kStageBytes + C::kABytes;
-          if (MODE == kGateUp) {
-            tma_load_3d(&tmB0, &full[s], sB, kb * BK, w.nb * 128, w.e);
-            tma_load_3d(&tmB1, &full[s], sB + 128 * BK, kb * BK, w.nb * 128, w.e);
-          } else {
 #pragma unroll
-            for (int i = 0; i < BN / 128; ++i)
-              tma_load_3d(&tmB0, &full[s], sB + i * 128 * BK, kb * BK, w.nb * BN + i * 128, w.e);
-          }
+          for (int i = 0; i < BN / 128; ++i)
+            tma_load_3d(MODE == kGateUp && i == 1 ? &tmB1 : &tmB0, &full[s], sB + i * 128 * BK,
+                        kb * BK, MODE == kGateUp ? w.nb * 128 : w.nb * BN + i * 128, w.e);
         };
         auto load_a = [&](int kb, int s) {
           uint8_t* sA = smem + s * C::kStageBytes;
-          if (big) {
-            tma_load_2d(&tmA128, &full[s], sA, kb * BK, w.row0);
-          } else {
-            for (int i = 0; i < nbox; ++i)
-              tma_load_2d(&tmA, &full[s], sA + i * kSmallBox * BK, kb * BK,
-                          w.row0 + i * kSmallBox);
-          }
+          for (int i = 0; i < nbox; ++i)
+            tma_load_2d(big ? &tmA128 : &tmA, &full[s], sA + i * box * BK, kb * BK,
+                        w.row0 + i * box);
         };
         int kb = 0;
         if (dep_pending) {
@@ -328,7 +369,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           // kernel that writes the rows, then their rows
           for (; kb < STAGES && kb < KB; ++kb) {
             if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
-            mbar_arrive_expect_tx(&full[stage], bytes);
             load_b(kb, stage);
             ++filled;
             if (++stage == STAGES) { stage = 0; phase ^= 1; }
@@ -340,7 +380,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (; kb < KB; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag)) { ok = false; break; }
-          mbar_arrive_expect_tx(&full[stage], bytes);
           load_b(kb, stage);
           load_a(kb, stage);
           ++filled;
@@ -398,51 +437,59 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     // ------------------------------------------------------ epilogue
+    // Warp: the token rows of TMEM lane quarter `quarter`, half of the columns:
+    // 128 of y, or 64 of g and the same 64 of u.
     const int quarter = warp & 3, half = warp >> 2;
-    constexpr int NC = BN / 2;  // columns per thread
+    constexpr int NC = BN / 2;  // sums per thread
     const int row = quarter * 32 + lane;
-    const bool has_lb = !(a.lbeta == 0.0f || a.lbeta != a.lbeta);
-    const float b_eff = (a.beta == 0.0f || a.beta != a.beta) ? 1.0f : a.beta;
+    const Act act = make_act(a.act_kind, a.beta, a.lbeta);
+    const uint32_t t_lane = tmem_base + ((uint32_t)(quarter * 32) << 16);
     if (a.early) pdl_wait();
     int buf = 0;
     uint32_t tphase = 0, parity = 0;
     bool ok = true;
     for (int64_t u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
       const Unit w = unit_of(u);
-      const bool warp_live = quarter * 32 < w.nrows;
-      const bool live = row < w.nrows;
-      const int64_t grow = (int64_t)w.row0 + row;
-      // scales of K block b: the row's, and the one or two of the columns
-      const float* sxp = a.xs + (live ? grow : (int64_t)w.row0) * KB;
+      const int rows = w.nrows - quarter * 32;  // this warp's (<= 0: none)
+      const int64_t row0 = (int64_t)w.row0 + quarter * 32;
+      const bool live = lane < rows;
+      // scales of a K block: the row's, times the one or two of the columns
+      const float* sxp = a.xs + (live ? row0 + lane : (int64_t)w.row0) * KB;
       int sb = w.nb;
       if (MODE == kPlain && BN == 256) sb = 2 * w.nb + half < NB ? 2 * w.nb + half : NB - 1;
       const float* w0p = a.ws0 + ((int64_t)w.e * NB + sb) * KB;
-      const float* w1p = MODE == kGateUp ? a.ws1 + ((int64_t)w.e * NB + sb) * KB : nullptr;
+      const float* w1p = MODE == kGateUp ? a.ws1 + ((int64_t)w.e * NB + sb) * KB : w0p;
+      // those of four K blocks, and of the next four, in flight meanwhile
+      float sx[4], s0[4], s1[4], nx[4], n0[4], n1[4];
+      auto fetch = [&](int k0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int b = k0 + j < KB ? k0 + j : KB - 1;
+          nx[j] = __ldg(sxp + b);
+          n0[j] = __ldg(w0p + b);
+          if (MODE == kGateUp) n1[j] = __ldg(w1p + b);
+        }
+      };
+      fetch(0);
       uint64_t acc2[NC / 2];  // the sums of columns 2i and 2i + 1
 #pragma unroll
       for (int i = 0; i < NC / 2; ++i) acc2[i] = 0;
-      // scales are fetched kAhead blocks before their use
-      constexpr int kAhead = 4;
-      float sxr[kAhead], w0r[kAhead], w1r[kAhead];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int b = j < KB ? j : KB - 1;
-        sxr[j] = __ldg(sxp + b);
-        w0r[j] = __ldg(w0p + b);
-        w1r[j] = MODE == kGateUp ? __ldg(w1p + b) : 0.0f;
-      }
       for (int kb = 0; kb < KB; ++kb) {
-        const uint64_t c0 = pair_of(sxr[0] * w0r[0]), c1 = pair_of(sxr[0] * w1r[0]);
+        if ((kb & 3) == 0) {
 #pragma unroll
-        for (int j = 0; j + 1 < kAhead; ++j) {
-          sxr[j] = sxr[j + 1];
-          w0r[j] = w0r[j + 1];
-          w1r[j] = w1r[j + 1];
+          for (int j = 0; j < 4; ++j) {
+            sx[j] = nx[j];
+            s0[j] = n0[j];
+            s1[j] = n1[j];
+          }
+          fetch(kb + 4);
         }
-        const int b = kb + kAhead < KB ? kb + kAhead : KB - 1;
-        sxr[kAhead - 1] = __ldg(sxp + b);
-        w0r[kAhead - 1] = __ldg(w0p + b);
-        if (MODE == kGateUp) w1r[kAhead - 1] = __ldg(w1p + b);
+        auto pick = [&](const float* v) {
+          return (kb & 2) ? ((kb & 1) ? v[3] : v[2]) : ((kb & 1) ? v[1] : v[0]);
+        };
+        const float fx = pick(sx);
+        const uint64_t c0 = pair_of(fx * pick(s0));
+        const uint64_t c1 = MODE == kGateUp ? pair_of(fx * pick(s1)) : c0;
         if (!__all_sync(0xffffffffu, mbar_wait(&tfull[buf], tphase, abort_flag))) {
           if (lane == 0) record_error(a.st, MOE_ERR_DEVICE_TIMEOUT, 330 + MODE);
           *abort_flag = 1;
@@ -450,16 +497,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        if (warp_live) {
-          const uint32_t t0 = tmem_base + ((uint32_t)(quarter * 32) << 16) + buf * BN;
+        if (rows > 0) {
 #pragma unroll
           for (int c = 0; c < NC; c += 32) {
             // gate_up: the thread's first 64 sums are g (w1), the next 64 u (w3)
             const bool second = MODE == kGateUp && c >= 64;
-            const uint32_t col = MODE == kGateUp ? (second ? 128 : 0) + 64 * half + (c & 63)
-                                                 : half * NC + c;
             uint32_t r[32];
-            sm100::tmem_ld32(t0 + col, r);
+            sm100::tmem_ld32(t_lane + buf * BN + (MODE == kGateUp ? (second ? 128 : 0) + 64 * half + (c & 63)
+                                                   : half * NC + c), r);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               fma2(acc2[c / 2 + i], r[2 * i], r[2 * i + 1], second ? c1 : c0);
@@ -471,50 +516,80 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++buf == C::kBufs) { buf = 0; tphase ^= 1; }
       }
       if (!ok) break;
-      float acc[NC];
+      if constexpr (MODE == kPlain) {
+        // kOutCols columns at a time through shared memory, so that a store
+        // covers whole sectors of few rows (each lane's own row, 16 bytes at a
+        // time, took 6,000 cycles a unit); a row's 16-byte words are permuted
+        // against bank conflicts.  The residual comes the same way.
+        constexpr int kW = C::kOutCols / 8;  // 16-byte words per row
+        constexpr int kRowsAt = 32 / kW;     // rows per warp-wide access
+        uint8_t* ob = out_x + warp * C::kOutBytes;
+        auto word = [&](int r, int j) {
+          return reinterpret_cast<uint4*>(ob + r * (16 * kW) + 16 * (j ^ ((r >> 1) & 3)));
+        };
+        const int n_first = w.nb * BN + NC * half;
 #pragma unroll
-      for (int i = 0; i < NC / 2; ++i) {
-        acc[2 * i] = lo_of(acc2[i]);
-        acc[2 * i + 1] = hi_of(acc2[i]);
-      }
-      if (MODE == kPlain) {
-        const int n0 = w.nb * BN + half * NC;
-        __nv_bfloat16* dst = a.y + grow * a.N + n0;
-        const __nv_bfloat16* rsrc = a.res ? a.res + grow * a.N + n0 : nullptr;
-        if (live) {
+        for (int c = 0; c < NC; c += C::kOutCols) {
+          const int n = n_first + c + 8 * (lane % kW);  // of this lane's accesses to y
+          const bool in = n < a.N;                      // N is a multiple of 8
+          if (a.res) {
 #pragma unroll
-          for (int c = 0; c < NC; c += 8) {
-            if (n0 + c < a.N) {  // N is a multiple of 8
-              float v[8];
+            for (int i = 0; i < kW; ++i) {
+              const int r = i * kRowsAt + lane / kW;
+              if (in && r < rows)
+                *word(r, lane % kW) =
+                    *reinterpret_cast<const uint4*>(a.res + (row0 + r) * a.N + n);
+            }
+            __syncwarp();
+          }
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = acc[c + i];
-              if (rsrc) {
-                const uint4 t = *reinterpret_cast<const uint4*>(rsrc + c);
-                const uint32_t tw[4] = {t.x, t.y, t.z, t.w};
+          for (int j = 0; j < kW; ++j) {
+            float v[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  v[2 * i] += __uint_as_float(tw[i] << 16);
-                  v[2 * i + 1] += __uint_as_float(tw[i] & 0xffff0000u);
-                }
-              }
-              uint32_t o[4];
+            for (int i = 0; i < 4; ++i) {
+              v[2 * i] = lo_of(acc2[c / 2 + 4 * j + i]);
+              v[2 * i + 1] = hi_of(acc2[c / 2 + 4 * j + i]);
+            }
+            if (a.res) {
+              const uint4 t = *word(lane, j);
+              const uint32_t tw[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                o[i] = *reinterpret_cast<const uint32_t*>(&p);
+                v[2 * i] += __uint_as_float(tw[i] << 16);
+                v[2 * i + 1] += __uint_as_float(tw[i] & 0xffff0000u);
               }
-              *reinterpret_cast<uint4*>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
             }
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+              o[i] = *reinterpret_cast<const uint32_t*>(&p);
+            }
+            *word(lane, j) = make_uint4(o[0], o[1], o[2], o[3]);
           }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < kW; ++i) {
+            const int r = i * kRowsAt + lane / kW;
+            if (in && r < rows)
+              *reinterpret_cast<uint4*>(a.y + (row0 + r) * a.N + n) = *word(r, lane % kW);
+          }
+          __syncwarp();
         }
       } else {
+        float acc[NC];
+#pragma unroll
+        for (int i = 0; i < NC / 2; ++i) {
+          acc[2 * i] = lo_of(acc2[i]);
+          acc[2 * i + 1] = hi_of(acc2[i]);
+        }
         // h of 64 columns in acc[0..63]; the block's largest |h| needs the
         // other half's too: exchanged through shared memory (the buffer
         // alternates, so a fast warp's next unit cannot overwrite it)
         uint32_t m = 0;  // magnitudes as integers, NaN above infinity
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
-          acc[i] = act32(acc[i], acc[64 + i], a.act_kind, b_eff, a.lbeta, has_lb);
+          acc[i] = act32(acc[i], acc[64 + i], act);
           m = max(m, __float_as_uint(acc[i]) & 0x7fffffffu);
         }
         uint32_t* xch = reinterpret_cast<uint32_t*>(amax_x) + parity * 2 * BM;
@@ -532,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float s = fp8::block_scale(__uint_as_float(m), a.pow2, inv);
         const int f0 = w.nb * 128 + 64 * half;
         if (live) {
-          uint8_t* dst = a.hq + grow * a.N + f0;
+          uint8_t* dst = a.hq + (row0 + lane) * a.N + f0;
 #pragma unroll
           for (int c = 0; c < 64; c += 16) {
             if (f0 + c < a.N) {  // N is a multiple of 16
@@ -544,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint4*>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
             }
           }
-          if (half == 0) a.hs[grow * NB + w.nb] = s;
+          if (half == 0) a.hs[(row0 + lane) * NB + w.nb] = s;
         }
       }
     }
@@ -597,26 +672,6 @@ struct DecCfg {
   static_assert(kTmem <= 512 && (kTmem & (kTmem - 1)) == 0, "TMEM columns");
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void st_cluster_f32(const void* local, uint32_t rank, float v) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(r), "f"(v) : "memory");
-}
 
 template <int MODE, int STAGES, int KSUB, bool SPLIT>
 __global__ void __launch_bounds__(kDecThreads, 1)
@@ -794,8 +849,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
   } else {
     // ------------------------------------------------------ epilogue
-    const bool has_lb = !(a.lbeta == 0.0f || a.lbeta != a.lbeta);
-    const float b_eff = (a.beta == 0.0f || a.beta != a.beta) ? 1.0f : a.beta;
+    const Act act = make_act(a.act_kind, a.beta, a.lbeta);
     const uint32_t lanes0 = tmem_base + ((uint32_t)(warp * 32) << 16);
     float* sc = scale_x + warp * 2 * C::kTiles * kNt;
     if (a.early) pdl_wait();
@@ -906,7 +960,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
         for (int i = 0; i < kNt; ++i) {
           if (i < w.nrows) {
-            acc[0][i] = act32(acc[0][i], acc[C::kTiles - 1][i], a.act_kind, b_eff, a.lbeta, has_lb);
+            acc[0][i] = act32(acc[0][i], acc[C::kTiles - 1][i], act);
             const uint32_t v =
                 __reduce_max_sync(0xffffffffu, __float_as_uint(acc[0][i]) & 0x7fffffffu);
             if (lane == i) mine = v;
@@ -1019,11 +1073,11 @@ int64_t max_tiles(const Args& a, int tile) {
   return a.S / tile + (a.S < a.E ? a.S : a.E);
 }
 
-template <int MODE, int BN, int STAGES>
+template <int MODE, int BN>
 cudaError_t launch(const CUtensorMap& b0, const CUtensorMap& b1, const CUtensorMap& a16,
                    const CUtensorMap& a128, const Args& args, cudaStream_t s) {
-  using C = Cfg<MODE, BN, STAGES>;
-  constexpr auto kernel = k_gemm_fp8<MODE, BN, STAGES>;
+  using C = Cfg<MODE, BN>;
+  constexpr auto kernel = k_gemm_fp8<MODE, BN>;
   static std::once_flag once[kMaxDevices];
   static cudaError_t set_up[kMaxDevices];
   const cudaError_t e = once_per_device(once, set_up, [&](int) {
@@ -1098,6 +1152,59 @@ int max_clusters(unsigned c) {
   return most[dev][c == 8 ? 3 : c == 4 ? 2 : 1];
 }
 
+// The variant of a product, by an estimate of its time from the sizes alone, with
+// segments taken as equally long: the waves of units over the SMs, times what a
+// unit costs, its K blocks and its end.  In microseconds, measured on a B200:
+//   decode          0.36 a K block with at most 16 rows a tile, 0.42 with more, 1.0
+//                   at the end; gate_up 0.70, 0.74 and 1.0;
+//   decode, split   the same and 4 for the cluster's launch and barriers;
+//   BN = 128        0.55 and 1.2;
+//   BN = 256        0.74 and 2.0, gate_up 0.74 and 2.5.
+// Some borders, measured on both sides (us): 32 segments, K = 2048, N = 7168:
+// decode against 256 rows 84 and 94 with 8 rows each, 108 and 100 with 32, 178
+// and 103 with 40.  One segment, K = 7168, N = 2048: decode split 8 ways, 128
+// and 256 rows 12, 32 and 44 with 16 rows; 46, 30 and 40 with 384; 149, 58 and
+// 42 with 2048.  K = N = 512, 64 rows: split 10.8, 128 rows 5.4.
+struct Choice {
+  int variant;        // 0 decode, 1 BN = 128, 2 BN = 256
+  unsigned clusters;  // decode: CTAs that share a unit's K
+};
+
+Choice choose(const Args& a, bool gate_up) {
+  const int sms = dev_info()->sm_count;
+  const int64_t KB = (a.K + BK - 1) / BK, NB = (a.N + 127) / 128;
+  const int64_t segs = !a.offsets ? 1 : a.S < a.E ? a.S : a.E;
+  const int64_t rows = (a.S + segs - 1) / segs;
+  auto tiles = [&](int tile) { return segs * ((rows + tile - 1) / tile); };
+  auto cost = [&](int64_t units, int64_t kbs, double per_kb, double end) {
+    return (double)((units + sms - 1) / sms) * ((double)kbs * per_kb + end);
+  };
+  Choice c{0, 1};
+  const double dec = gate_up ? (rows <= 16 ? 0.70 : 0.74) : (rows <= 16 ? 0.36 : 0.42);
+  double best = cost(tiles(kNt) * NB, KB, dec, 1.0);
+  if (!gate_up) {
+    // every cluster has one unit at most, all can run at once, and each CTA has
+    // a K block
+    const int64_t most = max_tiles(a, kNt) * NB;
+    for (unsigned k = 2; k <= 8 && most * k <= sms && KB >= k && most <= max_clusters(k); k *= 2) {
+      const double t = cost(most * k, (KB + k - 1) / k, dec, 5.0);
+      if (t < best) {
+        best = t;
+        c.clusters = k;
+      }
+    }
+    const double t = cost(tiles(BM) * NB, KB, 0.55, 1.2);
+    if (t < best) {
+      best = t;
+      c.variant = 1;
+    }
+  }
+  const double t = gate_up ? cost(tiles(BM) * NB, KB, 0.74, 2.5)
+                           : cost(tiles(BM) * ((a.N + 255) / 256), KB, 0.74, 2.0);
+  if (t < best) c.variant = 2;
+  return c;
+}
+
 struct Operands {
   const uint8_t* xq;
   const uint8_t* w0;
@@ -1106,31 +1213,31 @@ struct Operands {
 
 template <int MODE>
 int run_product(const Operands& o, const Args& args, cudaStream_t s) {
-  const int sms = dev_info()->sm_count;
+  const Choice c = choose(args, MODE == kGateUp);
   CUtensorMap w0, w1, t, t128;
   if (!map_weights(&w0, o.w0, args.K, args.N, args.E) ||
       !map_rows(&t, o.xq, args.K, args.S, kSmallBox))
     return MOE_ERR_CUDA;
   if (MODE == kGateUp && !map_weights(&w1, o.w1, args.K, args.N, args.E)) return MOE_ERR_CUDA;
+  const CUtensorMap& v1 = MODE == kGateUp ? w1 : w0;
   cudaError_t e;
-  if (args.S <= 16 * (int64_t)args.E) {
+  if (c.variant == 0) {
+    const int sms = dev_info()->sm_count;
     const int64_t units = max_tiles(args, kNt) * ((args.N + 127) / 128);
     const unsigned grid = (unsigned)(units < sms ? units : sms);
-    if constexpr (MODE == kGateUp) {
+    if constexpr (MODE == kGateUp)
       e = launch_dec<MODE, 3, 2, false>(w0, w1, t, args, grid, 1, s);
-    } else {
-      // a unit's K shared by a cluster while that fills more SMs, every cluster
-      // can run at once and each CTA keeps at least two K blocks
-      const int KB = (args.K + BK - 1) / BK;
-      unsigned c = 1;
-      while (c < 8 && units * c * 2 <= sms && KB >= 4 * (int)c && units <= max_clusters(2 * c))
-        c *= 2;
-      e = c > 1 ? launch_dec<MODE, 5, 2, true>(w0, w0, t, args, (unsigned)units * c, c, s)
-                : launch_dec<MODE, 5, 2, false>(w0, w0, t, args, grid, 1, s);
-    }
+    else
+      e = c.clusters > 1 ? launch_dec<MODE, 5, 2, true>(w0, w0, t, args, (unsigned)units * c.clusters,
+                                                        c.clusters, s)
+                         : launch_dec<MODE, 5, 2, false>(w0, w0, t, args, grid, 1, s);
   } else {
     if (!map_rows(&t128, o.xq, args.K, args.S, BM)) return MOE_ERR_CUDA;
-    e = launch<MODE, 256, 4>(w0, MODE == kGateUp ? w1 : w0, t, t128, args, s);
+    if constexpr (MODE == kGateUp)
+      e = launch<MODE, 256>(w0, v1, t, t128, args, s);
+    else
+      e = c.variant == 1 ? launch<MODE, 128>(w0, v1, t, t128, args, s)
+                         : launch<MODE, 256>(w0, v1, t, t128, args, s);
   }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -191,6 +191,7 @@ SEGMENTS = {
     "ragged": [16, 17, 0, 33, 129, 128, 127, 1],
     "tiles": [64, 256, 257, 31],
     "none": [0, 0, 0],
+    "large": [700, 300, 130, 513, 0],
 }
 
 
@@ -277,7 +278,7 @@ def make_ffn(g, E, d, F, S, pow2):
                                             ("situ", 0.0, 0.0)])
 @pytest.mark.parametrize("d,F,pow2", [(256, 128, False), (272, 400, True), (128, 16, False),
                                       (1040, 528, True)])
-@pytest.mark.parametrize("name", ["empty_ends", "ragged", "tiles"])
+@pytest.mark.parametrize("name", ["empty_ends", "ragged", "tiles", "large"])
 def test_expert_ffn_fp8(moe, name, d, F, pow2, act, beta, lbeta):
     counts = SEGMENTS[name]
     E = len(counts)
@@ -406,7 +407,7 @@ def test_fp8_results_repeat(moe):
         assert torch.equal(bits(y), bits(moe.linear_fp8(xq[:1], xs[:1], w[0][0], w[1][0])))
 
 
-@pytest.mark.parametrize("counts", [[3, 2, 0, 1], [300, 40, 0, 200]])
+@pytest.mark.parametrize("counts", [[3, 2, 0, 1], [300, 40, 0, 200], [900, 40, 300, 200]])
 def test_wait_probe_stops_the_8_bit_kernels(moe, counts):
     """The bounded wait that the diagnostics hook makes run out: an error status,
     outputs unwritten, and the next call as always."""
