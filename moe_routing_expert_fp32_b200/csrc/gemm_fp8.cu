@@ -165,15 +165,28 @@ __device__ __forceinline__ void tanh_parts(float x, float& num, float& den) {
   num = small ? p : copysignf(e - 1.0f, x);
   den = small ? 1.0f : e + 1.0f;
 }
-__device__ __forceinline__ float act32(float g, float u, const Act& t) {
-  const float sig = __fdividef(1.0f, 1.0f + __expf(-g));
-  if (!t.situ) return g * sig * u;
-  float n1, d1;
-  tanh_parts(g * t.inv_beta, n1, d1);
-  if (!t.has_lb) return t.beta * __fdividef(n1, d1) * sig * u;
-  float n2, d2;
-  tanh_parts(u * t.inv_lbeta, n2, d2);
-  return t.beta * t.lbeta * __fdividef(n1 * n2, d1 * d2) * sig;
+__device__ __forceinline__ float sigmoid32(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// f(h function): one copy of the caller's loop for each activation, so that the
+// choice is not made per element.
+template <typename F>
+__device__ __forceinline__ void with_act(const Act& t, F&& f) {
+  if (!t.situ) {
+    f([](float g, float u) { return g * sigmoid32(g) * u; });
+  } else if (!t.has_lb) {
+    f([&](float g, float u) {
+      float n, d;
+      tanh_parts(g * t.inv_beta, n, d);
+      return t.beta * __fdividef(n, d) * sigmoid32(g) * u;
+    });
+  } else {
+    const float bb = t.beta * t.lbeta;
+    f([&](float g, float u) {
+      float n1, d1, n2, d2;
+      tanh_parts(g * t.inv_beta, n1, d1);
+      tanh_parts(u * t.inv_lbeta, n2, d2);
+      return bb * __fdividef(n1 * n2, d1 * d2) * sigmoid32(g);
+    });
+  }
 }
 
 // Token tiles of `tile` rows per segment and their prefix into tile_start
@@ -348,13 +361,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool big = w.nrows > 2 * kSmallBox;
         const int box = big ? BM : kSmallBox;
         const int nbox = (w.nrows + box - 1) / box;
-        const uint32_t bytes = C::kBBytes + nbox * box * BK;
+        // (a narrow last block needs only its 128-row box)
+        const bool second = BN == 256 && (MODE == kGateUp || w.nb * BN + 128 < a.N);
+        const uint32_t bytes = (second ? 256 : 128) * BK + nbox * box * BK;
         auto load_b = [&](int kb, int s) {
           mbar_arrive_expect_tx(&full[s], bytes);
           uint8_t* sB = smem + s * C::kStageBytes + C::kABytes;
 #pragma unroll
           for (int i = 0; i < BN / 128; ++i)
-            tma_load_3d(MODE == kGateUp && i == 1 ? &tmB1 : &tmB0, &full[s], sB + i * 128 * BK,
+            if (i == 0 || second) tma_load_3d(MODE == kGateUp && i == 1 ? &tmB1 : &tmB0, &full[s], sB + i * 128 * BK,
                         kb * BK, MODE == kGateUp ? w.nb * 128 : w.nb * BN + i * 128, w.e);
         };
         auto load_a = [&](int kb, int s) {
@@ -402,9 +417,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0, buf = 0;
       uint32_t phase = 0, tphase = 0;
       bool ok = true;
-      const uint32_t idesc = idesc_e4m3(BM, BN);
       const uint64_t desc0 = sm100::smem_desc(smem_u32(smem), 1024, 2);
       for (int64_t u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
+        // the last block of columns may be narrower
+        const int cols = MODE == kPlain ? a.N - (int)(u % RB) * BN : BN;
+        const uint32_t idesc = idesc_e4m3(BM, cols < BN ? (cols + 15) / 16 * 16 : BN);
         for (int kb = 0; kb < KB; ++kb) {
           if (!mbar_wait(&tempty[buf], tphase ^ 1, abort_flag) ||
               !mbar_wait(&full[stage], phase, abort_flag)) {
@@ -453,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = w.nrows - quarter * 32;  // this warp's (<= 0: none)
       const int64_t row0 = (int64_t)w.row0 + quarter * 32;
       const bool live = lane < rows;
+      const int cols = MODE == kPlain ? a.N - w.nb * BN - half * NC : NC;  // of this warp that exist
       // scales of a K block: the row's, times the one or two of the columns
       const float* sxp = a.xs + (live ? row0 + lane : (int64_t)w.row0) * KB;
       int sb = w.nb;
@@ -500,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rows > 0) {
 #pragma unroll
           for (int c = 0; c < NC; c += 32) {
+            if (MODE == kPlain && c >= cols) break;
             // gate_up: the thread's first 64 sums are g (w1), the next 64 u (w3)
             const bool second = MODE == kGateUp && c >= 64;
             uint32_t r[32];
@@ -587,11 +606,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // other half's too: exchanged through shared memory (the buffer
         // alternates, so a fast warp's next unit cannot overwrite it)
         uint32_t m = 0;  // magnitudes as integers, NaN above infinity
+        with_act(act, [&](auto h) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          acc[i] = act32(acc[i], acc[64 + i], act);
-          m = max(m, __float_as_uint(acc[i]) & 0x7fffffffu);
-        }
+          for (int i = 0; i < 64; ++i) {
+            acc[i] = h(acc[i], acc[64 + i]);
+            m = max(m, __float_as_uint(acc[i]) & 0x7fffffffu);
+          }
+        });
         uint32_t* xch = reinterpret_cast<uint32_t*>(amax_x) + parity * 2 * BM;
         xch[half * BM + row] = m;
         __syncwarp();
@@ -605,22 +626,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         parity ^= 1;
         float inv;
         const float s = fp8::block_scale(__uint_as_float(m), a.pow2, inv);
-        const int f0 = w.nb * 128 + 64 * half;
-        if (live) {
-          uint8_t* dst = a.hq + (row0 + lane) * a.N + f0;
+        // the warp's 32 x 64 bytes through shared memory, as in the plain form
+        uint8_t* ob = out_x + warp * C::kOutBytes;
+        static_assert(C::kOutBytes == 32 * 64, "32 rows of 64 bytes");
+        auto word = [&](int r, int j) {
+          return reinterpret_cast<uint4*>(ob + r * 64 + 16 * (j ^ ((r >> 1) & 3)));
+        };
 #pragma unroll
-          for (int c = 0; c < 64; c += 16) {
-            if (f0 + c < a.N) {  // N is a multiple of 16
-              uint32_t o[4];
+        for (int j = 0; j < 4; ++j) {
+          uint32_t o[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                o[i] = fp8::pack4(acc[c + 4 * i] * inv, acc[c + 4 * i + 1] * inv,
-                                  acc[c + 4 * i + 2] * inv, acc[c + 4 * i + 3] * inv);
-              *reinterpret_cast<uint4*>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float* v = acc + 16 * j + 4 * i;
+            o[i] = fp8::pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
           }
-          if (half == 0) a.hs[(row0 + lane) * NB + w.nb] = s;
+          *word(lane, j) = make_uint4(o[0], o[1], o[2], o[3]);
         }
+        __syncwarp();
+        const int f = w.nb * 128 + 64 * half + 16 * (lane & 3);  // of this lane's stores
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * i + (lane >> 2);
+          if (r < rows && f < a.N)  // N is a multiple of 16
+            *reinterpret_cast<uint4*>(a.hq + (row0 + r) * a.N + f) = *word(r, lane & 3);
+        }
+        if (live && half == 0) a.hs[(row0 + lane) * NB + w.nb] = s;
+        __syncwarp();
       }
     }
   }  // roles
@@ -957,15 +988,17 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         // overwrite what a slow one still reads)
         uint32_t mine = 0;  // lane i: the warp's largest magnitude of token row i
         uint32_t* mx = max_x + parity * 4 * kNt;
+        with_act(act, [&](auto h) {
 #pragma unroll
-        for (int i = 0; i < kNt; ++i) {
-          if (i < w.nrows) {
-            acc[0][i] = act32(acc[0][i], acc[C::kTiles - 1][i], act);
-            const uint32_t v =
-                __reduce_max_sync(0xffffffffu, __float_as_uint(acc[0][i]) & 0x7fffffffu);
-            if (lane == i) mine = v;
+          for (int i = 0; i < kNt; ++i) {
+            if (i < w.nrows) {
+              acc[0][i] = h(acc[0][i], acc[C::kTiles - 1][i]);
+              const uint32_t v =
+                  __reduce_max_sync(0xffffffffu, __float_as_uint(acc[0][i]) & 0x7fffffffu);
+              if (lane == i) mine = v;
+            }
           }
-        }
+        });
         mx[warp * kNt + lane] = mine;
         __syncwarp();
         if (lane == 0) mbar_arrive(hmax);

@@ -42,8 +42,8 @@ __device__ __forceinline__ uint2 quant8(const uint4& v, float inv) {
   return make_uint2(pack4(f[0], f[1], f[2], f[3]), pack4(f[4], f[5], f[6], f[7]));
 }
 
-// Eight lanes per block of 128 columns: lane l holds columns 8l .. 8l+7 and
-// 64 + 8l .. 64 + 8l + 7, so every load and store of the eight is contiguous.
+// Eight lanes per block of 128 columns, 16 columns each (two 16-byte loads, one
+// 16-byte store).
 // SCATTER: row t goes to the `top_k` rows pos[t * top_k + k] (a dispatched
 // token; -1 where the slot was left out).  Its values are read and quantised
 // before the wait on the kernel before (the sort, which writes only pos).
@@ -71,11 +71,14 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const __nv_bfloat16* __re
     row = b / KB;
     kb = (int)(b - row * KB);
   }
-  const int c0 = kb * 128 + 8 * l8, c1 = c0 + 64;
-  const __nv_bfloat16* src = x + row * K;
+  const int c = kb * 128 + 16 * l8;
+  const bool in = live && c < K;  // K is a multiple of 16
+  const uint4* src = reinterpret_cast<const uint4*>(x + row * K + c);
   uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-  if (live && c0 < K) v0 = __ldg(reinterpret_cast<const uint4*>(src + c0));
-  if (live && c1 < K) v1 = __ldg(reinterpret_cast<const uint4*>(src + c1));
+  if (in) {
+    v0 = __ldg(src);
+    v1 = __ldg(src + 1);
+  }
   uint32_t m2 = amax8(amax8(0u, v0), v1);
   uint32_t m = max(m2 >> 16, m2 & 0xffffu);
 #pragma unroll
@@ -86,9 +89,7 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const __nv_bfloat16* __re
   if (SCATTER) pdl_wait();
   if (!live) return;
   auto store = [&](int64_t r) {
-    uint8_t* dst = q + r * K;
-    if (c0 < K) *reinterpret_cast<uint2*>(dst + c0) = q0;
-    if (c1 < K) *reinterpret_cast<uint2*>(dst + c1) = q1;
+    if (in) *reinterpret_cast<uint4*>(q + r * K + c) = make_uint4(q0.x, q0.y, q1.x, q1.y);
     if (l8 == 0) scale[r * KB + kb] = s;
   };
   if (SCATTER) {
