@@ -469,11 +469,13 @@ MOE_API int moe_block_forward(const moe_bf16* x, int64_t N, const moe_block_dims
  *   weights [B, N, K] carry one scale per 128 x 128 block,
  *     scale [B, ceil(N/128), ceil(K/128)].
  * Blocks at the ends may be partial.  Limits: K (the contracted width) a
- * multiple of 16, N (an output width) a multiple of 8; e4m3 and bf16 pointers
- * 16-byte aligned, scales 4-byte aligned.  Scales are the caller's: any fp32
- * values, not only those that moe_quantize_fp8 gives.  Products are summed in
- * fp32: 128 columns of K in the tensor core, times the two scales, then over
- * the blocks; one rounding to bf16 at the end. */
+ * multiple of 16, N (an output width) a multiple of 8, both at most 2^30; E at
+ * most 1024; e4m3 and bf16 pointers 16-byte aligned, scales 4-byte aligned.
+ * Scales are the caller's: any fp32 values, not only those that
+ * moe_quantize_fp8 gives.  Products are summed in fp32: 128 columns of K in the
+ * tensor core, times the product of the two scales (itself rounded to fp32),
+ * then over the blocks in order; one rounding to bf16 at the end.  A call's
+ * results depend on its arguments alone, bit for bit. */
 typedef uint8_t moe_fp8; /* e4m3 bit pattern (no infinities, NaN 0x7f) */
 
 /* bf16 to the 8-bit format.  x [B, M, K] bf16; q [B, M, K] e4m3.

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 from dataclasses import dataclass
 
@@ -248,9 +249,15 @@ def set_wait_probe(on: bool) -> bool:
 
 
 # ----------------------------------------------------------------- helpers
+_torch_mod = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_mod
+    if _torch_mod is None:
+        import torch
+        _torch_mod = torch
+    return _torch_mod
 
 
 def _stream():
@@ -661,25 +668,28 @@ def _fp8_args(*named):
     device, of that dtype and shape (None: any).  Returns the device's index."""
     dev = named[0][1].get_device()
     for name, t, dtype, shape in named:
+        if (t.dtype is dtype and t.get_device() == dev and dev >= 0 and t.is_contiguous() and
+                (shape is None or t.shape == shape)):
+            continue
         if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
         if shape is not None and t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, {named[0][0]} on cuda:{dev}")
+        raise ValueError(f"{name} is on {t.device}, {named[0][0]} on {named[0][1].device}")
     return dev
 
 
 def _fp8_call(fn: str, dev: int, *args):
     """Calls fn(*args, stream) on the current stream of device `dev`, which is made
     current for the call when it is not."""
-    C = _torch()._C
+    C = _torch_mod._C
     if C._cuda_getDevice() == dev:
-        code = getattr(lib(), fn)(*args, C._cuda_getCurrentRawStream(dev))
+        code = getattr(_lib or lib(), fn)(*args, C._cuda_getCurrentRawStream(dev))
     else:
-        with _torch().cuda.device(dev):
-            code = getattr(lib(), fn)(*args, C._cuda_getCurrentRawStream(dev))
-    _check(fn, code)
+        with _torch_mod.cuda.device(dev):
+            code = getattr(_lib or lib(), fn)(*args, C._cuda_getCurrentRawStream(dev))
+    if code != 0:
+        raise MoeError(fn, code)
 
 
 def _ws_for(ws, need, dev):
@@ -738,23 +748,24 @@ def quantize_fp8(x, block_rows: int = 1, pow2_scales: bool = False, q=None, scal
     if block_rows == 1:
         if len(shape) < 1:
             raise ValueError("x needs at least one dimension")
-        B, K = 1, shape[-1]
-        M = x.numel() // K if K else 0
-        s_shape = (*shape[:-1], _c128(K))
+        *lead, K = shape
+        B, M = 1, math.prod(lead)
+        s_shape = (*lead, (K + 127) // 128)
     else:
         if len(shape) not in (2, 3):
             raise ValueError("x must be [N, K] or [E, N, K] with block_rows = 128")
-        M, K = shape[-2], shape[-1]
-        B = shape[0] if len(shape) == 3 else 1
-        s_shape = (*shape[:-2], _c128(M), _c128(K))
-    named = [("x", x, torch.bfloat16, None)]
-    if q is not None:
-        named.append(("q", q, torch.float8_e4m3fn, shape))
-    if scale is not None:
-        named.append(("scale", scale, torch.float32, s_shape))
-    dev = _fp8_args(*named)
-    q = torch.empty_like(x, dtype=torch.float8_e4m3fn) if q is None else q
-    scale = x.new_empty(s_shape, dtype=torch.float32) if scale is None else scale
+        *lead, M, K = shape
+        B = lead[0] if lead else 1
+        s_shape = (*lead, (M + 127) // 128, (K + 127) // 128)
+    dev = _fp8_args(("x", x, torch.bfloat16, None))
+    if q is None:
+        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    else:
+        _fp8_args(("x", x, torch.bfloat16, None), ("q", q, torch.float8_e4m3fn, shape))
+    if scale is None:
+        scale = x.new_empty(s_shape, dtype=torch.float32)
+    else:
+        _fp8_args(("x", x, torch.bfloat16, None), ("scale", scale, torch.float32, s_shape))
     _fp8_call("moe_quantize_fp8", dev, x.data_ptr(), B, M, K, block_rows, int(pow2_scales),
               q.data_ptr(), scale.data_ptr())
     return q, scale

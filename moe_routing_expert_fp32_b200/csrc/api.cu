@@ -618,6 +618,7 @@ int64_t ceil128(int64_t v) { return (v + 127) / 128; }
 int check_fp8_product(int64_t S, int K, int E, int N) {
   if (S < 0 || K <= 0 || E < 1 || N <= 0) return MOE_ERR_INVALID_ARG;
   if (E > 1024 || K % 16 != 0 || N % 8 != 0 || S > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (K > (1 << 30) || N > (1 << 30)) return MOE_ERR_UNSUPPORTED;  // 32-bit column indexes
   return MOE_OK;
 }
 
@@ -644,7 +645,7 @@ int moe_quantize_fp8(const moe_bf16* x, int64_t B, int64_t M, int K, int block_r
                      int pow2_scales, moe_fp8* q, float* scale, void* stream) {
   if (B < 0 || M < 0 || K <= 0 || (block_rows != 1 && block_rows != 128))
     return MOE_ERR_INVALID_ARG;
-  if (K % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (K % 16 != 0 || K > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   if (B > INT32_MAX || M > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   const int64_t row_blocks = B * (block_rows == 1 ? M : ceil128(M));  // < 2^62
   if (row_blocks > INT32_MAX * (int64_t)(block_rows == 1 ? 16 : 1) / ceil128(K))
@@ -670,7 +671,7 @@ int moe_dispatch_fp8(const int32_t* topk_idx, int64_t N, int K, int E, const moe
                      void* stream) {
   if (N < 0 || K < 1 || E < 1 || d_e <= 0) return MOE_ERR_INVALID_ARG;
   if (E > 1024 || K > 16) return MOE_ERR_UNSUPPORTED;
-  if (d_e % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (d_e % 16 != 0 || d_e > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   if (N > INT32_MAX / K) return MOE_ERR_UNSUPPORTED;
   if (!counts || !offsets) return MOE_ERR_INVALID_ARG;
   if (N > 0 && (!topk_idx || !perm || !pos || !x_e || !xq || !x_scale)) return MOE_ERR_INVALID_ARG;

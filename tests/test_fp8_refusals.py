@@ -23,7 +23,7 @@ def mem():
 @pytest.mark.parametrize("B,M,K,rows,code", [
     (-1, 4, 128, 1, -1), (1, -4, 128, 1, -1), (1, 4, 0, 1, -1), (1, 4, 128, 64, -1),
     (1, 4, 120, 1, -2), (2 ** 40, 4, 128, 1, -2), (1, 2 ** 40, 128, 1, -2),
-    (2 ** 31 - 1, 2 ** 31 - 1, 7168, 1, -2), (2 ** 31 - 1, 2 ** 31 - 1, 16, 128, -2),
+    (1, 4, 2 ** 30 + 16, 1, -2), (2 ** 31 - 1, 2 ** 31 - 1, 7168, 1, -2), (2 ** 31 - 1, 2 ** 31 - 1, 16, 128, -2),
     (1, 4, 128, 1, -1)])  # the last: null pointers
 def test_quantize_refusals(m, B, M, K, rows, code):
     assert m.lib().moe_quantize_fp8(None, B, M, K, rows, 0, None, None, None) == code
@@ -49,7 +49,8 @@ def test_dispatch_refusals(m, N, K, E, d, code):
 @pytest.mark.parametrize("S,K,E,N,code", [
     (-1, 128, 4, 128, -1), (4, 0, 4, 128, -1), (4, 128, 0, 128, -1), (4, 128, 4, 0, -1),
     (4, 136, 4, 128, -2), (4, 128, 1025, 128, -2), (4, 128, 4, 12, -2),
-    (2 ** 31, 128, 4, 128, -2), (4, 128, 4, 128, -1)])
+    (2 ** 31, 128, 4, 128, -2), (4, 2 ** 30 + 16, 4, 128, -2), (4, 128, 4, 2 ** 30 + 8, -2),
+    (4, 128, 4, 128, -1)])
 def test_grouped_refusals(m, S, K, E, N, code):
     L, n = m.lib(), None
     assert L.moe_grouped_linear_fp8(n, n, n, E, S, K, n, n, N, n, n, 0, n) == code

@@ -117,7 +117,7 @@ def test_dispatch_fp8_leaves_out_bad_indices(moe):
 @pytest.mark.parametrize("M,K,N", [
     (1, 16, 8), (1, 7168, 2048), (2, 128, 128), (16, 2048, 1000), (17, 144, 136), (31, 272, 264),
     (33, 1040, 24), (100, 512, 384), (128, 1024, 256), (129, 400, 520), (300, 2048, 1160),
-    (1000, 1296, 640)])
+    (1000, 1296, 640), (5, 7168, 8), (40, 4096, 136), (3000, 400, 4232), (2048, 1040, 2312)])
 def test_linear_fp8(moe, M, K, N):
     g = gen(M + K + N)
     xq, xs = R.rand_rows(g, M, K)
@@ -405,6 +405,78 @@ def test_fp8_results_repeat(moe):
     y = moe.linear_fp8(xq[:1], xs[:1], w[0][0], w[1][0])
     for _ in range(3):
         assert torch.equal(bits(y), bits(moe.linear_fp8(xq[:1], xs[:1], w[0][0], w[1][0])))
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 2048, 1024), (64, 512, 512), (2048, 512, 4096)])
+def test_wait_probe_stops_the_8_bit_linear(moe, M, K, N):
+    """The same in the cluster-split decode kernel and both widths of the large one."""
+    g = gen(12)
+    xq, xs = R.rand_rows(g, M, K)
+    w, ws = R.rand_weights(g, 1, N, K)
+    good = moe.linear_fp8(xq, xs, w[0], ws[0])
+    wk = moe.workspace(256)
+    y = torch.full((M, N), 2.0, dtype=torch.bfloat16, device="cuda")
+    prev = moe.set_wait_probe(True)
+    try:
+        moe.linear_fp8(xq, xs, w[0], ws[0], out=y, ws=wk)
+        assert moe.get_status(wk) == -6
+    finally:
+        moe.set_wait_probe(prev)
+    assert (y == 2.0).all()
+    moe.linear_fp8(xq, xs, w[0], ws[0], out=y, ws=wk)
+    assert moe.get_status(wk) == 0 and torch.equal(bits(y), bits(good))
+
+
+def test_fp8_calls_back_to_back_and_on_two_streams(moe):
+    """Dependent calls without a synchronisation between them (each kernel is a
+    programmatic dependent of the one before), and independent ones at once on
+    two streams, each with its own workspace."""
+    g = gen(13)
+    S, E, d, F = 700, 6, 256, 128
+    off, _ = offsets_of([100, 0, 300, 1, 99, 200])
+    xq, xs, w = make_ffn(g, E, d, F, S, False)
+    act = moe.ActConfig("silu")
+    y = moe.expert_ffn_fp8(xq, xs, off, *w, act)
+    torch.cuda.synchronize()
+    chain = [y]
+    for _ in range(4):  # the output, quantised, is the next input
+        q, s = moe.quantize_fp8(chain[-1])
+        chain.append(moe.expert_ffn_fp8(q, s, off, *w, act))
+    torch.cuda.synchronize()
+    for a, b in zip(chain, chain[1:]):
+        torch.cuda.synchronize()
+        q, s = moe.quantize_fp8(a)
+        torch.cuda.synchronize()
+        assert torch.equal(bits(b), bits(moe.expert_ffn_fp8(q, s, off, *w, act)))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        for st, o in zip(streams, outs):
+            with torch.cuda.stream(st):
+                o.append(moe.expert_ffn_fp8(xq, xs, off, *w, act))
+    torch.cuda.synchronize()
+    for o in outs:
+        for t in o:
+            assert torch.equal(bits(t), bits(y))
+
+
+def test_linear_fp8_views_and_offsets_into_buffers(moe):
+    """Row slices of larger tensors: contiguous, 16-byte aligned, not at the start
+    of their allocation; the rows around the output stay as they were."""
+    g = gen(14)
+    xq, xs = R.rand_rows(g, 90, 272)
+    w, ws = R.rand_weights(g, 3, 200, 272)
+    out = torch.full((120, 200), 9.0, dtype=torch.bfloat16, device="cuda")
+    moe.linear_fp8(xq[7:77], xs[7:77], w[1], ws[1], out=out[20:90])
+    ref, bound = R.product(xq[7:77], xs[7:77], w[1], ws[1])
+    R.assert_within(out[20:90], ref, bound)
+    assert (out[:20] == 9).all() and (out[90:] == 9).all()
+    with pytest.raises(ValueError):
+        moe.linear_fp8(xq[::2], xs[::2], w[1], ws[1])
+    with pytest.raises(ValueError):
+        moe.linear_fp8(xq, xs, w[1], ws[1][:, :2])
 
 
 @pytest.mark.parametrize("counts", [[3, 2, 0, 1], [300, 40, 0, 200], [900, 40, 300, 200]])
