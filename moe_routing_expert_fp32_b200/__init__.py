@@ -1,7 +1,7 @@
 """Python binding of libmoe.so, the B200 (sm_100a) inference MoE layer.
 
-Argument marshalling only: every step of the layer runs in the library's CUDA
-kernels.  Tensors are torch CUDA tensors (PyTorch provides device memory and
+Argument marshalling only (ctypes; compiled for the 8-bit entry points): every
+step of the layer runs in the library's CUDA kernels.  Tensors are torch CUDA tensors (PyTorch provides device memory and
 streams); every call enqueues on ``torch.cuda.current_stream()`` and returns
 without synchronising.  The entry points and their semantics are those of
 ``include/moe.h``.
@@ -12,8 +12,6 @@ binding's functions raises.
 from __future__ import annotations
 
 import ctypes
-import functools
-import math
 import os
 from dataclasses import dataclass
 
@@ -249,15 +247,9 @@ def set_wait_probe(on: bool) -> bool:
 
 
 # ----------------------------------------------------------------- helpers
-_torch_mod = None
-
-
 def _torch():
-    global _torch_mod
-    if _torch_mod is None:
-        import torch
-        _torch_mod = torch
-    return _torch_mod
+    import torch
+    return torch
 
 
 def _stream():
@@ -661,79 +653,26 @@ def block_forward(x, weights: BlockWeights, cfg: RouteConfig, act: ActConfig, no
 
 
 # ------------------------------------------------- 8-bit block-scaled forms
-# These calls take a few microseconds on the GPU at decode sizes, so the
-# marshalling is kept short: raw pointers, the raw stream, one pass of checks.
-def _fp8_args(*named):
-    """Checks (name, tensor, dtype, shape) entries: contiguous CUDA tensors of one
-    device, of that dtype and shape (None: any).  Returns the device's index."""
-    dev = named[0][1].get_device()
-    for name, t, dtype, shape in named:
-        if (t.dtype is dtype and t.get_device() == dev and dev >= 0 and t.is_contiguous() and
-                (shape is None or t.shape == shape)):
-            continue
-        if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
-        if shape is not None and t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        raise ValueError(f"{name} is on {t.device}, {named[0][0]} on {named[0][1].device}")
-    return dev
+# These calls take a few microseconds on the GPU at decode sizes; their checks,
+# allocations and marshalling are compiled (csrc/torch_binding.cpp).
+_ext = None
 
 
-def _fp8_call(fn: str, dev: int, *args):
-    """Calls fn(*args, stream) on the current stream of device `dev`, which is made
-    current for the call when it is not."""
-    C = _torch_mod._C
-    if C._cuda_getDevice() == dev:
-        code = getattr(_lib or lib(), fn)(*args, C._cuda_getCurrentRawStream(dev))
-    else:
-        with _torch_mod.cuda.device(dev):
-            code = getattr(_lib or lib(), fn)(*args, C._cuda_getCurrentRawStream(dev))
-    if code != 0:
-        raise MoeError(fn, code)
+def _binding():
+    """The compiled calls (raises if they or libmoe.so have not been built)."""
+    global _ext
+    if _ext is None:
+        lib()
+        _torch()
+        from . import _torch_binding
+        _ext = _torch_binding
+    return _ext
 
 
-def _ws_for(ws, need, dev):
-    if ws is None:
-        torch = _torch()
-        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    if ws.get_device() != dev:
-        raise ValueError(f"ws is on {ws.device}, expected cuda:{dev}")
-    return ws
-
-
-_status_only = {}  # device index -> 256 bytes
-
-
-def _status_ws(ws, dev):
-    """The workspace of a call that needs only the status word: the caller's, or
-    one that the calls of a device share (nothing reads its status)."""
-    if ws is not None:
-        return _ws_for(ws, 0, dev)
-    w = _status_only.get(dev)
-    if w is None:
-        torch = _torch()
-        w = torch.empty(256, dtype=torch.uint8, device=dev)
-        if not torch.cuda.is_current_stream_capturing():  # not memory of a graph's pool
-            _status_only[dev] = w
-    return w
-
-
-@functools.lru_cache(maxsize=256)
-def _dispatch_ws(N, K, E):
-    return lib().moe_dispatch_workspace_size(N, K, E)
-
-
-@functools.lru_cache(maxsize=256)
-def _ffn_fp8_ws(S, d, E, F):
-    return lib().moe_expert_ffn_fp8_workspace_size(S, d, E, F)
-
-
-def _opt(t):
-    return None if t is None else t.data_ptr()
-
-
-def _c128(n):
-    return (n + 127) // 128
+def _result(fn: str, r):
+    if type(r) is int:
+        raise MoeError(fn, r)
+    return r
 
 
 def quantize_fp8(x, block_rows: int = 1, pow2_scales: bool = False, q=None, scale=None):
@@ -743,79 +682,24 @@ def quantize_fp8(x, block_rows: int = 1, pow2_scales: bool = False, q=None, scal
     scale [..., ceil(K/128)].  block_rows 128 (weights): x [N, K] or
     [E, N, K], one scale per 128 x 128 block, scale [..., ceil(N/128),
     ceil(K/128)].  pow2_scales rounds the scales up to powers of two."""
-    torch = _torch()
-    shape = x.shape
-    if block_rows == 1:
-        if len(shape) < 1:
-            raise ValueError("x needs at least one dimension")
-        *lead, K = shape
-        B, M = 1, math.prod(lead)
-        s_shape = (*lead, (K + 127) // 128)
-    else:
-        if len(shape) not in (2, 3):
-            raise ValueError("x must be [N, K] or [E, N, K] with block_rows = 128")
-        *lead, M, K = shape
-        B = lead[0] if lead else 1
-        s_shape = (*lead, (M + 127) // 128, (K + 127) // 128)
-    dev = _fp8_args(("x", x, torch.bfloat16, None))
-    if q is None:
-        q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
-    else:
-        _fp8_args(("x", x, torch.bfloat16, None), ("q", q, torch.float8_e4m3fn, shape))
-    if scale is None:
-        scale = x.new_empty(s_shape, dtype=torch.float32)
-    else:
-        _fp8_args(("x", x, torch.bfloat16, None), ("scale", scale, torch.float32, s_shape))
-    _fp8_call("moe_quantize_fp8", dev, x.data_ptr(), B, M, K, block_rows, int(pow2_scales),
-              q.data_ptr(), scale.data_ptr())
-    return q, scale
+    return _result("moe_quantize_fp8",
+                   (_ext or _binding()).quantize_fp8(x, block_rows, pow2_scales, q, scale))
 
 
 def dispatch_fp8(topk_idx, x_e, num_experts: int, pow2_scales: bool = False, ws=None):
     """dispatch() with the rows quantised as they are gathered
     (moe_dispatch_fp8): (counts [E], offsets [E+1], perm [S], pos [S],
     xq [S, d_e] e4m3, x_scale [S, ceil(d_e/128)])."""
-    torch = _torch()
-    N, K = topk_idx.shape
-    d_e = x_e.shape[1]
-    E, S = num_experts, N * K
-    dev = _fp8_args(("x_e", x_e, torch.bfloat16, (N, d_e)),
-                    ("topk_idx", topk_idx, torch.int32, None))
-    need = _dispatch_ws(N, K, E)
-    # one allocation for the integers and, at its start, the workspace
-    at = 0 if ws is not None else (need + 255) // 256 * 64
-    ints = x_e.new_empty(at + 2 * E + 1 + 2 * S, dtype=torch.int32)
-    own_ws, counts, offsets, perm, pos = ints.split((at, E, E + 1, S, S))
-    xq = x_e.new_empty((S, d_e), dtype=torch.float8_e4m3fn)
-    xs = x_e.new_empty((S, _c128(d_e)), dtype=torch.float32)
-    ws_p, ws_n = ((own_ws.data_ptr(), 4 * at) if ws is None else
-                  (_ws_for(ws, 0, dev).data_ptr(), ws.numel()))
-    _fp8_call("moe_dispatch_fp8", dev, topk_idx.data_ptr(), N, K, E, x_e.data_ptr(), d_e,
-              int(pow2_scales), counts.data_ptr(), offsets.data_ptr(), perm.data_ptr(),
-              pos.data_ptr(), xq.data_ptr(), xs.data_ptr(), ws_p, ws_n)
-    return counts, offsets, perm, pos, xq, xs
+    return _result("moe_dispatch_fp8",
+                   (_ext or _binding()).dispatch_fp8(topk_idx, x_e, num_experts, pow2_scales, ws))
 
 
 def linear_fp8(xq, x_scale, w, w_scale, residual=None, out=None, ws=None):
     """bf16(x . W^T (+ residual)) of 8-bit operands (moe_linear_fp8): xq [M, K],
     x_scale [M, ceil(K/128)], w [N_out, K], w_scale [ceil(N_out/128),
     ceil(K/128)]."""
-    torch = _torch()
-    M, K = xq.shape
-    N = w.shape[0]
-    f8, f32, bf = torch.float8_e4m3fn, torch.float32, torch.bfloat16
-    named = [("xq", xq, f8, None), ("x_scale", x_scale, f32, (M, _c128(K))),
-             ("w", w, f8, (N, K)), ("w_scale", w_scale, f32, (_c128(N), _c128(K)))]
-    if residual is not None:
-        named.append(("residual", residual, bf, (M, N)))
-    if out is not None:
-        named.append(("out", out, bf, (M, N)))
-    dev = _fp8_args(*named)
-    ws = _status_ws(ws, dev)  # moe_linear_fp8_workspace_size: the status word
-    out = xq.new_empty((M, N), dtype=bf) if out is None else out
-    _fp8_call("moe_linear_fp8", dev, xq.data_ptr(), x_scale.data_ptr(), M, K, w.data_ptr(),
-              w_scale.data_ptr(), N, _opt(residual), out.data_ptr(), ws.data_ptr(), ws.numel())
-    return out
+    return _result("moe_linear_fp8",
+                   (_ext or _binding()).linear_fp8(xq, x_scale, w, w_scale, residual, out, ws))
 
 
 def grouped_linear_fp8(xq, x_scale, offsets, w, w_scale, out=None, ws=None):
@@ -823,34 +707,12 @@ def grouped_linear_fp8(xq, x_scale, offsets, w, w_scale, out=None, ws=None):
     offsets[e+1]-1 (moe_grouped_linear_fp8): xq [S, K], w [E, N_out, K],
     w_scale [E, ceil(N_out/128), ceil(K/128)]; returns [S, N_out] bf16, whose
     rows from offsets[E] on are left as they were."""
-    torch = _torch()
-    S, K = xq.shape
-    E, N, _ = w.shape
-    f8, f32, bf = torch.float8_e4m3fn, torch.float32, torch.bfloat16
-    named = [("xq", xq, f8, None), ("x_scale", x_scale, f32, (S, _c128(K))),
-             ("offsets", offsets, torch.int32, (E + 1,)), ("w", w, f8, (E, N, K)),
-             ("w_scale", w_scale, f32, (E, _c128(N), _c128(K)))]
-    if out is not None:
-        named.append(("out", out, bf, (S, N)))
-    dev = _fp8_args(*named)
-    ws = _status_ws(ws, dev)  # moe_grouped_linear_fp8_workspace_size: the status word
-    out = xq.new_empty((S, N), dtype=bf) if out is None else out
-    _fp8_call("moe_grouped_linear_fp8", dev, xq.data_ptr(), x_scale.data_ptr(),
-              offsets.data_ptr(), E, S, K, w.data_ptr(), w_scale.data_ptr(), N, out.data_ptr(),
-              ws.data_ptr(), ws.numel())
-    return out
+    return _result("moe_grouped_linear_fp8",
+                   (_ext or _binding()).grouped_linear_fp8(xq, x_scale, offsets, w, w_scale, out,
+                                                           ws))
 
 
-def _fp8_experts(w1, w1_scale, w3, w3_scale, w2, w2_scale):
-    """The (name, tensor, dtype, shape) checks and the C struct of the 8-bit experts."""
-    torch = _torch()
-    E, F, d = w1.shape
-    f8, f32 = torch.float8_e4m3fn, torch.float32
-    up = (E, _c128(F), _c128(d))
-    named = [("w1", w1, f8, None), ("w1_scale", w1_scale, f32, up), ("w3", w3, f8, (E, F, d)),
-             ("w3_scale", w3_scale, f32, up), ("w2", w2, f8, (E, d, F)),
-             ("w2_scale", w2_scale, f32, (E, _c128(d), _c128(F)))]
-    return named, _Fp8Experts(*[t.data_ptr() for t in (w1, w3, w2, w1_scale, w3_scale, w2_scale)])
+_ACT_KIND = {"silu": MOE_ACT_SILU, "situ": MOE_ACT_SITU}
 
 
 def expert_ffn_fp8(xq, x_scale, offsets, w1, w1_scale, w3, w3_scale, w2, w2_scale, act: ActConfig,
@@ -858,26 +720,10 @@ def expert_ffn_fp8(xq, x_scale, offsets, w1, w1_scale, w3, w3_scale, w2, w2_scal
     """The expert MLP on 8-bit rows and weights (moe_expert_ffn_fp8): xq [S, d]
     sorted by expert, w1, w3 [E, F, d], w2 [E, d, F] with their block scales;
     returns [S, d] bf16, whose rows from offsets[E] on are left as they were."""
-    torch = _torch()
-    S, d = xq.shape
-    E, F, _ = w1.shape
-    named, xw = _fp8_experts(w1, w1_scale, w3, w3_scale, w2, w2_scale)
-    named += [("xq", xq, torch.float8_e4m3fn, (S, w1.shape[2])),
-              ("x_scale", x_scale, torch.float32, (S, _c128(d))),
-              ("offsets", offsets, torch.int32, (E + 1,))]
-    if y is not None:
-        named.append(("y", y, torch.bfloat16, (S, d)))
-    dev = _fp8_args(*named)
-    need = _ffn_fp8_ws(S, d, E, F)
-    if need == 0:
-        raise MoeError("moe_expert_ffn_fp8_workspace_size", -2)
-    ws = _ws_for(ws, need, dev)
-    y = xq.new_empty((S, d), dtype=torch.bfloat16) if y is None else y
-    a = act._c()
-    _fp8_call("moe_expert_ffn_fp8", dev, xq.data_ptr(), x_scale.data_ptr(), offsets.data_ptr(), E,
-              S, d, F, ctypes.byref(xw), ctypes.byref(a), int(pow2_scales), y.data_ptr(),
-              ws.data_ptr(), ws.numel())
-    return y
+    return _result("moe_expert_ffn_fp8",
+                   (_ext or _binding()).expert_ffn_fp8(
+                       xq, x_scale, offsets, w1, w1_scale, w3, w3_scale, w2, w2_scale,
+                       _ACT_KIND[act.kind], act.beta, act.linear_beta, pow2_scales, y, ws))
 
 
 def forward_fp8(x_r, W, bias, cfg: RouteConfig, w1, w1_scale, w3, w3_scale, w2, w2_scale,
@@ -886,31 +732,16 @@ def forward_fp8(x_r, W, bias, cfg: RouteConfig, w1, w1_scale, w3, w3_scale, w2, 
     """The routed MoE layer with 8-bit experts (moe_forward_fp8): route,
     dispatch_fp8, expert_ffn_fp8 and combine.  Arguments as forward(), with the
     experts' weights in the 8-bit format.  Returns ``out`` [N, d_e] bf16."""
-    torch = _torch()
-    N, d_r = x_r.shape
-    E, F, d_e = w1.shape
-    if E != cfg.num_experts:
-        raise ValueError("w1 does not hold num_experts experts")
-    if x_e is None and d_e != d_r:
-        raise ValueError("x_e is required when the experts' width differs from the router's")
-    named, xw = _fp8_experts(w1, w1_scale, w3, w3_scale, w2, w2_scale)
-    named += [("x_r", x_r, torch.bfloat16, None), ("W", W, torch.float32, (E, d_r))]
-    for name, t, dtype, shape in (("x_e", x_e, torch.bfloat16, (N, d_e)),
-                                  ("bias", bias, torch.float32, (E,)),
-                                  ("out", out, torch.bfloat16, (N, d_e)),
-                                  ("topk_idx", topk_idx, torch.int32, (N, cfg.top_k)),
-                                  ("topk_w", topk_w, torch.float32, (N, cfg.top_k))):
-        if t is not None:
-            named.append((name, t, dtype, shape))
-    dev = _fp8_args(*named)
-    c, a = cfg._c(), act._c()
-    need = lib().moe_forward_fp8_workspace_size(N, d_r, d_e, ctypes.byref(c), F)
-    if need == 0:
-        raise MoeError("moe_forward_fp8_workspace_size", -2)
-    ws = _ws_for(ws, need, dev)
-    out = torch.empty((N, d_e), dtype=torch.bfloat16, device=dev) if out is None else out
-    _fp8_call("moe_forward_fp8", dev, x_r.data_ptr(), _opt(x_e), N, d_r, d_e, W.data_ptr(),
-              _opt(bias), ctypes.byref(c), ctypes.byref(xw), F, ctypes.byref(a),
-              int(pow2_scales), out.data_ptr(), _opt(topk_idx), _opt(topk_w), ws.data_ptr(),
-              ws.numel())
-    return out
+    c = cfg._c()
+    return _result("moe_forward_fp8",
+                   (_ext or _binding()).forward_fp8(
+                       x_r, W, bias, c.num_experts, c.n_group, c.topk_group, c.top_k,
+                       c.norm_topk_prob, c.route_scale, c.score_func, c.group_score, w1, w1_scale,
+                       w3, w3_scale, w2, w2_scale, _ACT_KIND[act.kind], act.beta,
+                       act.linear_beta, x_e, pow2_scales, ws, out, topk_idx, topk_w))
+
+
+def forward_fp8_workspace_size(N: int, d_r: int, d_e: int, cfg: RouteConfig, F: int) -> int:
+    """Bytes of forward_fp8's workspace (0 for shapes it does not take)."""
+    c = cfg._c()
+    return int(lib().moe_forward_fp8_workspace_size(N, d_r, d_e, ctypes.byref(c), F))

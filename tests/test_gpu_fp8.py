@@ -366,9 +366,7 @@ def test_fp8_calls_on_a_side_stream_and_in_a_graph(moe):
     act = moe.ActConfig("silu")
     want = moe.forward_fp8(x, W, bias, cfg, *q, act).clone()
     want_neg = moe.forward_fp8(-x, W, bias, cfg, *q, act).clone()
-    need = moe.lib().moe_forward_fp8_workspace_size(
-        100, 256, 256, moe.ctypes.byref(cfg._c()), 128)
-    ws = moe.workspace(need)
+    ws = moe.workspace(moe.forward_fp8_workspace_size(100, 256, 256, cfg, 128))
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
