@@ -24,6 +24,8 @@
 // is bounded as in expert_gemm.cu.
 #include <cuda.h>
 
+#include <cuda_fp16.h>
+
 #include "fp8.cuh"
 #include "moe_internal.cuh"
 #include "sm100.cuh"
@@ -990,12 +992,15 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         uint32_t* mx = max_x + parity * 4 * kNt;
         with_act(act, [&](auto h) {
 #pragma unroll
-          for (int i = 0; i < kNt; ++i) {
-            if (i < w.nrows) {
-              acc[0][i] = h(acc[0][i], acc[C::kTiles - 1][i]);
-              const uint32_t v =
-                  __reduce_max_sync(0xffffffffu, __float_as_uint(acc[0][i]) & 0x7fffffffu);
-              if (lane == i) mine = v;
+          for (int i0 = 0; i0 < kNt; i0 += 8) {
+            if (i0 < w.nrows) {  // eight at a time: independent chains
+#pragma unroll
+              for (int i = i0; i < i0 + 8; ++i) {
+                acc[0][i] = h(acc[0][i], acc[C::kTiles - 1][i]);
+                const uint32_t v =
+                    __reduce_max_sync(0xffffffffu, __float_as_uint(acc[0][i]) & 0x7fffffffu);
+                if (lane == i) mine = v;
+              }
             }
           }
         });
@@ -1052,6 +1057,104 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     __syncwarp();
     tc_fence_after();
     sm100::tmem_dealloc(tmem_base, C::kTmem);
+  }
+}
+
+// ------------------------------------------------------------ few rows
+// A dense product of at most kFewRows rows: a matrix-vector product on the CUDA
+// cores.  One warp per weight row, 16 bytes a lane and step, so a step covers
+// 512 contiguous bytes, four K blocks, and eight lanes share a block: each lane
+// sums its 16 products in fp32, times sx * sw, over the steps, and the warp adds
+// its lanes at the end.  The rows of x are in shared memory as fp32.  There is
+// nothing to stage or hand over, so it ends in half the time of the decode
+// kernel, whose cluster and barriers cost more than the work: one row, K = 7168,
+// N = 2048: 10.4 us there.
+constexpr int kFewRows = 4;
+constexpr int kFewWarps = 16;
+constexpr int kFewMaxSmem = 128 * 1024;
+
+template <int M>
+__global__ void __launch_bounds__(32 * kFewWarps, 1)
+    k_linear_few(const uint8_t* __restrict__ w, const uint8_t* __restrict__ xq, const Args a) {
+  // x as it is read: float4 word i (0 .. 3) of lane l in step t of row m is
+  // x4[((m * steps + t) * 4 + i) * 32 + l], free of bank conflicts
+  extern __shared__ float4 x4[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int KB = (a.K + BK - 1) / BK, steps = (a.K + 511) / 512, words16 = a.K / 16;
+  pdl_wait();
+  pdl_trigger();
+  if (a.reset && blockIdx.x == 0 && threadIdx.x == 0) *a.st = DeviceStatus{0, 0};
+  auto two = [](uint32_t e4m3x2) {  // the lower two e4m3 as floats (exact)
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)e4m3x2));
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+  };
+  for (int i = threadIdx.x; i < M * words16; i += 32 * kFewWarps) {
+    const int m = i / words16, c = i - m * words16;
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(xq + (int64_t)m * a.K) + c);
+    const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 p = two(words[j]), q = two(words[j] >> 16);
+      x4[((m * steps + (c >> 5)) * 4 + j) * 32 + (c & 31)] = make_float4(p.x, p.y, q.x, q.y);
+    }
+  }
+  __syncthreads();
+  for (int n = blockIdx.x * kFewWarps + warp; n < a.N; n += gridDim.x * kFewWarps) {
+    const uint8_t* row = w + (int64_t)n * a.K;
+    const float* sw = a.ws0 + (int64_t)(n >> 7) * KB;
+    float acc[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) acc[m] = 0.0f;
+    constexpr int kBatch = 7;  // loads in flight per lane
+    for (int k0 = 16 * lane; k0 - 16 * lane < a.K; k0 += 512 * kBatch) {
+      uint4 v[kBatch];
+      float f[kBatch][M];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int k = k0 + 512 * j;
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (k < a.K) v[j] = __ldg(reinterpret_cast<const uint4*>(row + k));
+        const int b = k < a.K ? k >> 7 : KB - 1;
+        const float s = __ldg(sw + b);
+#pragma unroll
+        for (int m = 0; m < M; ++m) f[j][m] = s * __ldg(a.xs + (int64_t)m * KB + b);
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int k = k0 + 512 * j;
+        if (k >= a.K) break;
+        float p[M];
+#pragma unroll
+        for (int m = 0; m < M; ++m) p[m] = 0.0f;
+        const uint32_t words[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 lo = two(words[i]), hi = two(words[i] >> 16);
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            const float4 x = x4[((m * steps + (k >> 9)) * 4 + i) * 32 + lane];
+            p[m] = fmaf(lo.x, x.x, p[m]);
+            p[m] = fmaf(lo.y, x.y, p[m]);
+            p[m] = fmaf(hi.x, x.z, p[m]);
+            p[m] = fmaf(hi.y, x.w, p[m]);
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < M; ++m) acc[m] = fmaf(p[m], f[j][m], acc[m]);
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
+      if (lane == 0) {
+        const int64_t at = (int64_t)m * a.N + n;
+        float y = acc[m];
+        if (a.res) y += __bfloat162float(a.res[at]);
+        a.y[at] = __float2bfloat16_rn(y);
+      }
+    }
   }
 }
 
@@ -1185,21 +1288,27 @@ int max_clusters(unsigned c) {
   return most[dev][c == 8 ? 3 : c == 4 ? 2 : 1];
 }
 
+size_t few_smem(int64_t M, int K) { return (size_t)M * ((K + 511) / 512) * 512 * sizeof(float); }
+
 // The variant of a product, by an estimate of its time from the sizes alone, with
 // segments taken as equally long: the waves of units over the SMs, times what a
 // unit costs, its K blocks and its end.  In microseconds, measured on a B200:
 //   decode          0.36 a K block with at most 16 rows a tile, 0.42 with more, 1.0
 //                   at the end; gate_up 0.70, 0.74 and 1.0;
-//   decode, split   the same and 4 for the cluster's launch and barriers;
+//   decode, split   at the end 2.7 and 0.06 a row (the parts' exchange);
 //   BN = 128        0.55 and 1.2;
-//   BN = 256        0.74 and 2.0, gate_up 0.74 and 2.5.
+//   BN = 256        0.74 and 2.0, gate_up 0.74 and 2.5;
+//   few rows        0.12 + 0.14 a row for 512 columns of K, and 1.1 less than the
+//                   others to begin with.
 // Some borders, measured on both sides (us): 32 segments, K = 2048, N = 7168:
 // decode against 256 rows 84 and 94 with 8 rows each, 108 and 100 with 32, 178
-// and 103 with 40.  One segment, K = 7168, N = 2048: decode split 8 ways, 128
+// and 103 with 40.  One row, K = 7168: few rows against decode 5.1 and 10.5 with
+// N = 2048, 33 and 25 with N = 18944; three rows 9.6 and 10.6, four 11.7 and 10.6
+// with N = 2048.  One segment, K = 7168, N = 2048: decode split 8 ways, 128
 // and 256 rows 12, 32 and 44 with 16 rows; 46, 30 and 40 with 384; 149, 58 and
 // 42 with 2048.  K = N = 512, 64 rows: split 10.8, 128 rows 5.4.
 struct Choice {
-  int variant;        // 0 decode, 1 BN = 128, 2 BN = 256
+  int variant;        // 0 decode, 1 BN = 128, 2 BN = 256, 3 few rows
   unsigned clusters;  // decode: CTAs that share a unit's K
 };
 
@@ -1220,7 +1329,8 @@ Choice choose(const Args& a, bool gate_up) {
     // a K block
     const int64_t most = max_tiles(a, kNt) * NB;
     for (unsigned k = 2; k <= 8 && most * k <= sms && KB >= k && most <= max_clusters(k); k *= 2) {
-      const double t = cost(most * k, (KB + k - 1) / k, dec, 5.0);
+      const double t =
+          cost(most * k, (KB + k - 1) / k, dec, 2.7 + 0.06 * (double)(rows < kNt ? rows : kNt));
       if (t < best) {
         best = t;
         c.clusters = k;
@@ -1234,7 +1344,16 @@ Choice choose(const Args& a, bool gate_up) {
   }
   const double t = gate_up ? cost(tiles(BM) * NB, KB, 0.74, 2.5)
                            : cost(tiles(BM) * ((a.N + 255) / 256), KB, 0.74, 2.0);
-  if (t < best) c.variant = 2;
+  if (t < best) {
+    best = t;
+    c.variant = 2;
+  }
+  if (!gate_up && !a.offsets && a.S <= kFewRows && few_smem(a.S, a.K) <= kFewMaxSmem) {
+    const int64_t per_wave = (int64_t)sms * kFewWarps;
+    const double few = (double)((a.N + per_wave - 1) / per_wave) * ((a.K + 511) / 512) *
+                           (0.12 + 0.14 * (double)a.S) - 1.1;
+    if (few < best) c.variant = 3;
+  }
   return c;
 }
 
@@ -1244,9 +1363,31 @@ struct Operands {
   const uint8_t* w1;  // gate_up
 };
 
+template <int M>
+cudaError_t launch_few(const Operands& o, const Args& args, cudaStream_t s) {
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t set_up[kMaxDevices];
+  const cudaError_t e = once_per_device(once, set_up, [](int) {
+    return cudaFuncSetAttribute(k_linear_few<M>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kFewMaxSmem);
+  });
+  if (e != cudaSuccess) return e;
+  const int ctas = (args.N + kFewWarps - 1) / kFewWarps, sms = dev_info()->sm_count;
+  const size_t smem = few_smem(M, args.K);
+  return launch_pdl(k_linear_few<M>, dim3(ctas < sms ? ctas : sms), dim3(32 * kFewWarps), smem, s,
+                    o.w0, o.xq, args);
+}
+
 template <int MODE>
 int run_product(const Operands& o, const Args& args, cudaStream_t s) {
   const Choice c = choose(args, MODE == kGateUp);
+  if (c.variant == 3) {
+    const cudaError_t e = args.S == 1   ? launch_few<1>(o, args, s)
+                          : args.S == 2 ? launch_few<2>(o, args, s)
+                          : args.S == 3 ? launch_few<3>(o, args, s)
+                                        : launch_few<4>(o, args, s);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
   CUtensorMap w0, w1, t, t128;
   if (!map_weights(&w0, o.w0, args.K, args.N, args.E) ||
       !map_rows(&t, o.xq, args.K, args.S, kSmallBox))

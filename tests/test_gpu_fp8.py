@@ -117,7 +117,8 @@ def test_dispatch_fp8_leaves_out_bad_indices(moe):
 @pytest.mark.parametrize("M,K,N", [
     (1, 16, 8), (1, 7168, 2048), (2, 128, 128), (16, 2048, 1000), (17, 144, 136), (31, 272, 264),
     (33, 1040, 24), (100, 512, 384), (128, 1024, 256), (129, 400, 520), (300, 2048, 1160),
-    (1000, 1296, 640), (5, 7168, 8), (40, 4096, 136), (3000, 400, 4232), (2048, 1040, 2312)])
+    (1000, 1296, 640), (5, 7168, 8), (40, 4096, 136), (3, 1040, 72),
+    (4, 8192, 2056), (4, 8208, 520), (1, 32784, 40), (2, 7152, 5000), (3000, 400, 4232), (2048, 1040, 2312)])
 def test_linear_fp8(moe, M, K, N):
     g = gen(M + K + N)
     xq, xs = R.rand_rows(g, M, K)
@@ -405,7 +406,7 @@ def test_fp8_results_repeat(moe):
         assert torch.equal(bits(y), bits(moe.linear_fp8(xq[:1], xs[:1], w[0][0], w[1][0])))
 
 
-@pytest.mark.parametrize("M,K,N", [(1, 2048, 1024), (64, 512, 512), (2048, 512, 4096)])
+@pytest.mark.parametrize("M,K,N", [(8, 2048, 1024), (64, 512, 512), (2048, 512, 4096)])
 def test_wait_probe_stops_the_8_bit_linear(moe, M, K, N):
     """The same in the cluster-split decode kernel and both widths of the large one."""
     g = gen(12)
