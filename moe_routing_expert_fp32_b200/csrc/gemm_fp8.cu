@@ -932,19 +932,34 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         __syncwarp();  // the products sx * sw are in shared memory
         tc_fence_after();
+        const uint32_t t0 = lanes0 + buf * C::kBufCols;
+        if (w.nrows <= 8) {  // the usual decode step: a quarter of the columns
 #pragma unroll
-        for (int c = 0; c < kNt; c += 16) {
-          if (c < w.nrows) {
+          for (int t = 0; t < C::kTiles; ++t) {
+            uint32_t r[8];
+            sm100::tmem_ld8(t0 + t * kNt, r);
 #pragma unroll
-            for (int t = 0; t < C::kTiles; ++t) {
-              uint32_t r[16];
-              sm100::tmem_ld16(lanes0 + buf * C::kBufCols + t * kNt + c, r);
+            for (int i = 0; i < 8; i += 4) {
+              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(scp + t * kNt + i);
+              fma2(acc2[t][i / 2], r[i], r[i + 1], f.x);
+              fma2(acc2[t][i / 2 + 1], r[i + 2], r[i + 3], f.y);
+            }
+          }
+        } else {
 #pragma unroll
-              for (int i = 0; i < 16; i += 4) {
-                const ulonglong2 f =
-                    *reinterpret_cast<const ulonglong2*>(scp + t * kNt + c + i);
-                fma2(acc2[t][(c + i) / 2], r[i], r[i + 1], f.x);
-                fma2(acc2[t][(c + i) / 2 + 1], r[i + 2], r[i + 3], f.y);
+          for (int c = 0; c < kNt; c += 16) {
+            if (c < w.nrows) {
+#pragma unroll
+              for (int t = 0; t < C::kTiles; ++t) {
+                uint32_t r[16];
+                sm100::tmem_ld16(t0 + t * kNt + c, r);
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                  const ulonglong2 f =
+                      *reinterpret_cast<const ulonglong2*>(scp + t * kNt + c + i);
+                  fma2(acc2[t][(c + i) / 2], r[i], r[i + 1], f.x);
+                  fma2(acc2[t][(c + i) / 2 + 1], r[i + 2], r[i + 3], f.y);
+                }
               }
             }
           }
