@@ -79,7 +79,8 @@ struct Cfg {
   static constexpr int kOutCols = 32;  // columns that a warp stores at a time
   static constexpr int kOutBytes = 32 * kOutCols * 2;  // of a warp's 32 rows
   static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024 + kBarBytes +
-                                  kAmaxBytes + kEpiWarps * kOutBytes + kStartBytes;
+                                  kAmaxBytes + kEpiWarps * kOutBytes + 2 * kStartBytes;
+  static constexpr int kCache = kMaxSegments + 1;  // offsets held in shared memory
   static_assert(kABytes % 1024 == 0 && kBBytes % 1024 == 0, "1024-byte aligned operands");
   static_assert(MODE == kPlain || BN == 256, "gate_up: 128 rows of w1 and of w3");
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -195,88 +196,125 @@ __device__ __forceinline__ void with_act(const Act& t, F&& f) {
 // [E + 1] (shared memory), by every CTA for itself.  A segment that is not
 // inside [0, S] or runs backwards is recorded and gets no tile, so no row out
 // of range is touched.  Every thread of the CTA calls it, after the wait on the
-// kernel before; it ends with a __syncthreads.
-template <int THREADS>
-__device__ __forceinline__ void build_tiles(const Args& a, int tile, int32_t* tile_start,
-                                            int32_t* warp_tot) {
+// kernel before; it ends with a __syncthreads.  Returns the offsets: a copy in
+// `cache` (shared memory, CACHE entries), since every role looks them up for
+// every unit, or the caller's where they are too many.
+template <int THREADS, int CACHE>
+__device__ __forceinline__ const int32_t* build_tiles(const Args& a, int tile,
+                                                      int32_t* tile_start, int32_t* cache,
+                                                      int32_t* warp_tot) {
   constexpr int kPer = (kMaxSegments + THREADS) / THREADS;  // segments per thread, and E itself
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int e0 = kPer * threadIdx.x;
+  const int E = a.E;
   if (a.reset && blockIdx.x == 0) {
     // instead of a memset before the kernel; the other CTAs record nothing but
     // waits that have run out, long after this
     if (threadIdx.x == 0) *a.st = DeviceStatus{0, 0};
-    __syncthreads();
+    __syncwarp();  // (the first warp may record next; for the others, the barrier below)
   }
-  int32_t n[kPer], sum = 0;
+  if (E <= 128) {
+    // few segments (or one, of all rows): the first warp alone, four a lane
+    if (warp == 0) {
+      const int f0 = 4 * lane;
+      int32_t o[5], n4[4], sum = 0;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    n[i] = 0;
-    if (e0 + i < a.E) {
-      const int64_t lo = a.offsets ? a.offsets[e0 + i] : 0;
-      const int64_t hi = a.offsets ? a.offsets[e0 + i + 1] : a.S;
-      const bool bad = lo < 0 || hi < lo || hi > a.S || (e0 + i == 0 && lo != 0);
-      if (!bad) n[i] = (int32_t)((hi - lo + tile - 1) / tile);
-      else if (blockIdx.x == 0) record_error(a.st, MOE_ERR_DEVICE_BOUNDS, 300);
+      for (int i = 0; i < 5; ++i)
+        o[i] = f0 + i > E ? 0 : a.offsets ? a.offsets[f0 + i] : f0 + i ? (int32_t)a.S : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        n4[i] = 0;
+        if (f0 + i < E) {
+          const bool bad = o[i] < 0 || o[i + 1] < o[i] || o[i + 1] > a.S || (f0 + i == 0 && o[0]);
+          if (!bad) n4[i] = (int32_t)(((int64_t)o[i + 1] - o[i] + tile - 1) / tile);
+          else if (blockIdx.x == 0) record_error(a.st, MOE_ERR_DEVICE_BOUNDS, 300);
+        }
+        sum += n4[i];
+      }
+      int32_t x = sum;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int32_t t = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += t;
+      }
+      x -= sum;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        if (f0 + i <= E && (i < 4 || lane == 31)) {
+          tile_start[f0 + i] = x;
+          cache[f0 + i] = o[i];
+        }
+        if (i < 4) x += n4[i];
+      }
     }
-    sum += n[i];
+    __syncthreads();
+    return cache;
+  }
+  const int32_t* off = a.offsets;
+  if (E < CACHE) {
+    for (int e = threadIdx.x; e <= E; e += THREADS)
+      cache[e] = a.offsets[e];
+    off = cache;
+  }
+  __syncthreads();
+  const int e0 = kPer * threadIdx.x;
+  int32_t n[kPer], sum = 0;
+  if (e0 < E) {
+    int32_t lo = off[e0];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      n[i] = 0;
+      if (e0 + i < E) {
+        const int32_t hi = off[e0 + i + 1];
+        const bool bad = lo < 0 || hi < lo || hi > a.S || (e0 + i == 0 && lo != 0);
+        if (!bad) n[i] = (int32_t)(((int64_t)hi - lo + tile - 1) / tile);
+        else if (blockIdx.x == 0) record_error(a.st, MOE_ERR_DEVICE_BOUNDS, 300);
+        lo = hi;
+      }
+      sum += n[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) n[i] = 0;
   }
   int32_t x = sum;
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int32_t o = __shfl_up_sync(0xffffffffu, x, off);
-    if (lane >= off) x += o;
+  for (int off1 = 1; off1 < 32; off1 <<= 1) {
+    const int32_t o = __shfl_up_sync(0xffffffffu, x, off1);
+    if (lane >= off1) x += o;
   }
   if (lane == 31) warp_tot[warp] = x;
   __syncthreads();
   int32_t run = x - sum;
   for (int w = 0; w < warp; ++w) run += warp_tot[w];
+  if (e0 <= E) {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (e0 + i <= a.E) tile_start[e0 + i] = run;
-    run += n[i];
+    for (int i = 0; i < kPer; ++i) {
+      if (e0 + i <= E) tile_start[e0 + i] = run;
+      run += n[i];
+    }
   }
   __syncthreads();
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void st_cluster_f32(const void* local, uint32_t rank, float v) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(r), "f"(v) : "memory");
+  return off;
 }
 
 struct Unit {
   int e, row0, nrows, nb;
 };
 // Unit u: weight block u % RB of token tile u / RB.
-__device__ __forceinline__ Unit unit_at(const Args& a, const int32_t* tile_start, int RB, int tile,
-                                        int64_t u) {
+__device__ __forceinline__ Unit unit_at(int E, const int32_t* offsets, const int32_t* tile_start,
+                                        int RB, int tile, uint32_t u) {
   Unit r;
-  const int tt = (int)(u / RB);
-  r.nb = (int)(u - (int64_t)tt * RB);
-  int lo = 0, hi = a.E - 1;
+  const int tt = (int)(u / (uint32_t)RB);
+  r.nb = (int)(u - (uint32_t)tt * (uint32_t)RB);
+  int lo = 0, hi = E - 1;
   while (lo < hi) {  // largest e with tile_start[e] <= tt
     const int mid = (lo + hi + 1) >> 1;
     if (tile_start[mid] <= tt) lo = mid;
     else hi = mid - 1;
   }
   r.e = lo;
-  r.row0 = (a.offsets ? a.offsets[lo] : 0) + (tt - tile_start[lo]) * tile;
-  const int end = a.offsets ? a.offsets[lo + 1] : (int)a.S;
+  r.row0 = offsets[lo] + (tt - tile_start[lo]) * tile;
+  const int end = offsets[lo + 1];
   r.nrows = end - r.row0 < tile ? end - r.row0 : tile;
   return r;
 }
@@ -304,6 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* amax_x = reinterpret_cast<float*>(tail + kBarBytes);
   uint8_t* out_x = tail + kBarBytes + C::kAmaxBytes;
   int32_t* tile_start = reinterpret_cast<int32_t*>(out_x + kEpiWarps * C::kOutBytes);
+  int32_t* off_x = tile_start + kMaxSegments + 1;
   static_assert((2 * STAGES + 2 * C::kBufs + 6) * 8 + 8 <= kBarBytes, "barriers");
   __shared__ int32_t warp_tot[kThreads / 32];
 
@@ -338,12 +377,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!a.early) pdl_wait();
 
   tc_fence_before();
-  build_tiles<kThreads>(a, BM, tile_start, warp_tot);
+  const int32_t* off = build_tiles<kThreads, C::kCache>(a, BM, tile_start, off_x, warp_tot);
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int64_t total_units = (int64_t)tile_start[a.E] * RB;
+  const uint32_t total_units = (uint32_t)tile_start[a.E] * (uint32_t)RB;  // < 2^31
 
-  auto unit_of = [&](int64_t u) { return unit_at(a, tile_start, RB, BM, u); };
+  auto unit_of = [&](uint32_t u) { return unit_at(a.E, off, tile_start, RB, BM, u); };
 
   if (warp >= kEpiWarps) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
@@ -357,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (a.probe)  // the diagnostics hook: a wait that runs out
         ok = mbar_wait(never, 0, abort_flag, kProbeLimitNs);
       bool dep_pending = a.early != 0;
-      for (int64_t u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
+      for (uint32_t u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
         const Unit w = unit_of(u);
         // token rows: one box of 128, or 16-row boxes for a short tile
         const bool big = w.nrows > 2 * kSmallBox;
@@ -420,9 +459,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, tphase = 0;
       bool ok = true;
       const uint64_t desc0 = sm100::smem_desc(smem_u32(smem), 1024, 2);
-      for (int64_t u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
+      for (uint32_t u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
         // the last block of columns may be narrower
-        const int cols = MODE == kPlain ? a.N - (int)(u % RB) * BN : BN;
+        const int cols = MODE == kPlain ? a.N - (int)(u % (uint32_t)RB) * BN : BN;
         const uint32_t idesc = idesc_e4m3(BM, cols < BN ? (cols + 15) / 16 * 16 : BN);
         for (int kb = 0; kb < KB; ++kb) {
           if (!mbar_wait(&tempty[buf], tphase ^ 1, abort_flag) ||
@@ -467,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int buf = 0;
     uint32_t tphase = 0, parity = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
+    for (uint32_t u = blockIdx.x; u < total_units && ok; u += gridDim.x) {
       const Unit w = unit_of(u);
       const int rows = w.nrows - quarter * 32;  // this warp's (<= 0: none)
       const int64_t row0 = (int64_t)w.row0 + quarter * 32;
@@ -666,6 +705,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void st_cluster_f32(const void* local, uint32_t rank, float v) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(r), "f"(v) : "memory");
+}
+
 // --------------------------------------------------------- decode variant
 // A few rows per segment: the product is a stream of weights.  Here the weight
 // rows are the MMA's M side (128 of them; gate_up 128 of w1 and the same 128 of
@@ -700,8 +759,9 @@ struct DecCfg {
   static constexpr int kStartBytes = (kMaxSegments + 1) * 4;
   static constexpr int kMaxBytes = 2 * 4 * kNt * 4;  // gate_up: unit parity x warp x row
   static constexpr int kPartBytes = MODE == kPlain ? 128 * kNt * 4 : 0;  // SPLIT's partial sums
+  static constexpr int kCache = 640;  // offsets held in shared memory
   static constexpr size_t kSmem = (size_t)STAGES * kStageBytes + 1024 + kBarBytes + kScaleBytes +
-                                  kMaxBytes + kPartBytes + kStartBytes;
+                                  kMaxBytes + kPartBytes + kStartBytes + 4 * kCache;
   static_assert(kTmem <= 512 && (kTmem & (kTmem - 1)) == 0, "TMEM columns");
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -731,13 +791,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   float* part = reinterpret_cast<float*>(tail + kBarBytes + C::kScaleBytes + C::kMaxBytes);
   int32_t* tile_start = reinterpret_cast<int32_t*>(tail + kBarBytes + C::kScaleBytes +
                                                    C::kMaxBytes + C::kPartBytes);
+  int32_t* off_x = tile_start + kMaxSegments + 1;
   __shared__ int32_t warp_tot[kDecThreads / 32];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int KB = (a.K + BK - 1) / BK;
   const int NB = (a.N + 127) / 128;  // weight blocks = scale rows
   const uint32_t csize = SPLIT ? cluster_size() : 1, crank = SPLIT ? cluster_rank() : 0;
-  const int64_t unit0 = blockIdx.x / csize, unit_step = gridDim.x / csize;
+  const uint32_t unit0 = blockIdx.x / csize, unit_step = gridDim.x / csize;
   const int kb0 = (int)((int64_t)crank * KB / csize);
   const int kb1 = (int)((int64_t)(crank + 1) * KB / csize);
 
@@ -764,12 +825,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   if (warp == 5) sm100::tmem_alloc(tmem_slot, C::kTmem);
   if (!a.early) pdl_wait();
   tc_fence_before();
-  build_tiles<kDecThreads>(a, kNt, tile_start, warp_tot);
+  const int32_t* off = build_tiles<kDecThreads, C::kCache>(a, kNt, tile_start, off_x, warp_tot);
   tc_fence_after();
   if (SPLIT) cluster_sync();  // the other CTAs run: their shared memory may be written
   const uint32_t tmem_base = *tmem_slot;
-  const int64_t total_units = (int64_t)tile_start[a.E] * NB;
-  auto unit_of = [&](int64_t u) { return unit_at(a, tile_start, NB, kNt, u); };
+  const uint32_t total_units = (uint32_t)tile_start[a.E] * (uint32_t)NB;  // < 2^31
+  auto unit_of = [&](uint32_t u) { return unit_at(a.E, off, tile_start, NB, kNt, u); };
 
   if (warp == 4) {
     // ------------------------------------------------------ TMA producer
@@ -781,7 +842,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       bool ok = true;
       if (a.probe) ok = mbar_wait(never, 0, abort_flag, kProbeLimitNs);
       bool dep_pending = a.early != 0;
-      for (int64_t u = unit0; u < total_units && ok; u += unit_step) {
+      for (uint32_t u = unit0; u < total_units && ok; u += unit_step) {
         const Unit w = unit_of(u);
         const int nbox = (w.nrows + kSmallBox - 1) / kSmallBox;
         const uint32_t bytes = C::kWBytes + nbox * kSmallBox * BK;  // of a K block
@@ -845,7 +906,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       uint32_t phase = 0, tphase = 0;
       bool ok = true;
       const uint64_t desc0 = sm100::smem_desc(smem_u32(smem), 1024, 2);
-      for (int64_t u = unit0; u < total_units && ok; u += unit_step) {
+      for (uint32_t u = unit0; u < total_units && ok; u += unit_step) {
         const Unit w = unit_of(u);
         const uint32_t idesc = idesc_e4m3(128, (w.nrows + 15) / 16 * 16);
         for (int kb = kb0; kb < kb1 && ok; kb += KSUB) {
@@ -889,7 +950,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     int buf = 0;
     uint32_t tphase = 0, parity = 0;
     bool ok = true;
-    for (int64_t u = unit0; u < total_units && ok; u += unit_step) {
+    for (uint32_t u = unit0; u < total_units && ok; u += unit_step) {
       const Unit w = unit_of(u);
       // lane t fetches the scales of token row t, kAhead blocks before their use
       const float* sxp =
@@ -984,19 +1045,20 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         // weight row m is finished by CTA m / rpc of the cluster
         const int rpc = 128 / csize;
 #pragma unroll
-        for (int i = 0; i < kNt; ++i)
-          if (i < w.nrows)
-            st_cluster_f32(part + ((int)crank * kNt + i) * rpc + m % rpc, m / rpc, acc[0][i]);
+        for (int i = 0; i < kNt; ++i) {
+          if (i >= w.nrows) break;
+          st_cluster_f32(part + ((int)crank * kNt + i) * rpc + m % rpc, m / rpc, acc[0][i]);
+        }
       } else if (MODE == kPlain) {
         if (n < a.N) {
           const int64_t at = (int64_t)w.row0 * a.N + n;
 #pragma unroll
-          for (int i = 0; i < kNt; ++i)
-            if (i < w.nrows) {
-              float v = acc[0][i];
-              if (a.res) v += __bfloat162float(a.res[at + (int64_t)i * a.N]);
-              a.y[at + (int64_t)i * a.N] = __float2bfloat16_rn(v);
-            }
+          for (int i = 0; i < kNt; ++i) {
+            if (i >= w.nrows) break;
+            float v = acc[0][i];
+            if (a.res) v += __bfloat162float(a.res[at + (int64_t)i * a.N]);
+            a.y[at + (int64_t)i * a.N] = __float2bfloat16_rn(v);
+          }
         }
       } else {
         // h of one d_ff row and all token rows; the largest |h| of a token row
@@ -1007,15 +1069,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         uint32_t* mx = max_x + parity * 4 * kNt;
         with_act(act, [&](auto h) {
 #pragma unroll
-          for (int i0 = 0; i0 < kNt; i0 += 8) {
-            if (i0 < w.nrows) {  // eight at a time: independent chains
+          for (int i0 = 0; i0 < kNt; i0 += 8) {  // eight at a time: independent chains
+            if (i0 >= w.nrows) break;
 #pragma unroll
-              for (int i = i0; i < i0 + 8; ++i) {
-                acc[0][i] = h(acc[0][i], acc[C::kTiles - 1][i]);
-                const uint32_t v =
-                    __reduce_max_sync(0xffffffffu, __float_as_uint(acc[0][i]) & 0x7fffffffu);
-                if (lane == i) mine = v;
-              }
+            for (int i = i0; i < i0 + 8; ++i) {
+              acc[0][i] = h(acc[0][i], acc[C::kTiles - 1][i]);
+              const uint32_t v =
+                  __reduce_max_sync(0xffffffffu, __float_as_uint(acc[0][i]) & 0x7fffffffu);
+              if (lane == i) mine = v;
             }
           }
         });
@@ -1035,14 +1096,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         uint8_t* dst = a.hq + (int64_t)w.row0 * a.N + n;
 #pragma unroll
         for (int i = 0; i < kNt; i += 2) {
-          if (i < w.nrows) {
-            const float q0 = acc[0][i] * __shfl_sync(0xffffffffu, inv, i);
-            const float q1 = acc[0][i + 1] * __shfl_sync(0xffffffffu, inv, i + 1);
-            const uint32_t q = fp8::pack4(q0, q1, 0.0f, 0.0f);
-            if (n < a.N) {
-              dst[(int64_t)i * a.N] = (uint8_t)q;
-              if (i + 1 < w.nrows) dst[(int64_t)(i + 1) * a.N] = (uint8_t)(q >> 8);
-            }
+          if (i >= w.nrows) break;
+          const float q0 = acc[0][i] * __shfl_sync(0xffffffffu, inv, i);
+          const float q1 = acc[0][i + 1] * __shfl_sync(0xffffffffu, inv, i + 1);
+          const uint32_t q = fp8::pack4(q0, q1, 0.0f, 0.0f);
+          if (n < a.N) {
+            dst[(int64_t)i * a.N] = (uint8_t)q;
+            if (i + 1 < w.nrows) dst[(int64_t)(i + 1) * a.N] = (uint8_t)(q >> 8);
           }
         }
       }
@@ -1395,6 +1455,8 @@ cudaError_t launch_few(const Operands& o, const Args& args, cudaStream_t s) {
 
 template <int MODE>
 int run_product(const Operands& o, const Args& args, cudaStream_t s) {
+  // units are counted in 31 bits (more would be a terabyte of weights or outputs)
+  if (max_tiles(args, kNt) > INT32_MAX / ((args.N + 127) / 128)) return MOE_ERR_UNSUPPORTED;
   const Choice c = choose(args, MODE == kGateUp);
   if (c.variant == 3) {
     const cudaError_t e = args.S == 1   ? launch_few<1>(o, args, s)
