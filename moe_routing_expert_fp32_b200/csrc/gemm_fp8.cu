@@ -962,7 +962,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       for (int t = 0; t < C::kTiles; ++t)
 #pragma unroll
         for (int i = 0; i < kNt / 2; ++i) acc2[t][i] = 0;
-      constexpr int kAhead = 4;
+      constexpr int kAhead = 2;
       float sxr[kAhead], w0r[kAhead], w1r[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
