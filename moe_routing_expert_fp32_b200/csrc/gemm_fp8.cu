@@ -1368,20 +1368,21 @@ size_t few_smem(int64_t M, int K) { return (size_t)M * ((K + 511) / 512) * 512 *
 // The variant of a product, by an estimate of its time from the sizes alone, with
 // segments taken as equally long: the waves of units over the SMs, times what a
 // unit costs, its K blocks and its end.  In microseconds, measured on a B200:
-//   decode          0.36 a K block with at most 16 rows a tile, 0.42 with more, 1.0
+//   decode          0.33 a K block with at most 16 rows a tile, 0.36 with more, 1.0
 //                   at the end; gate_up 0.70, 0.74 and 1.0;
-//   decode, split   at the end 2.7 and 0.06 a row (the parts' exchange);
-//   BN = 128        0.55 and 1.2;
-//   BN = 256        0.74 and 2.0, gate_up 0.74 and 2.5;
-//   few rows        0.12 + 0.14 a row for 512 columns of K, and 1.1 less than the
-//                   others to begin with.
+//   decode, split   at the end 2.4 and 0.08 a row (the parts' exchange);
+//   BN = 128        0.45 and 1.2;
+//   BN = 256        0.72 and 2.0, gate_up 0.74 and 2.5;
+//   few rows        0.12 + 0.14 a row for 512 columns of K.
 // Some borders, measured on both sides (us): 32 segments, K = 2048, N = 7168:
-// decode against 256 rows 84 and 94 with 8 rows each, 108 and 100 with 32, 178
-// and 103 with 40.  One row, K = 7168: few rows against decode 5.1 and 10.5 with
-// N = 2048, 33 and 25 with N = 18944; three rows 9.6 and 10.6, four 11.7 and 10.6
-// with N = 2048.  One segment, K = 7168, N = 2048: decode split 8 ways, 128
-// and 256 rows 12, 32 and 44 with 16 rows; 46, 30 and 40 with 384; 149, 58 and
-// 42 with 2048.  K = N = 512, 64 rows: split 10.8, 128 rows 5.4.
+// decode against 256 rows 78 and 92 with 8 rows each, 86 and 96 with 32, 147
+// and 95 with 40; 16 segments, K = N = 512, 128 rows each: decode, 128 and 256
+// rows 7.6, 6.3 and 8.4.  Few rows against decode, K = 7168: one row 5.1 and 8.5
+// with N = 2048, 33 and 25 with N = 18944; two rows 7.2 and 8.5, three 9.5 and 8.5
+// with N = 2048.  One segment, K = 7168, N = 2048: decode split 4 ways, not
+// split, 128 and 256 rows 9.5, 21, 23 and 36 with 16 rows; decode, 128 and 256 rows
+// 41, 26 and 39 with 384; 135, 51 and 40 with 2048.  K = N = 512, 64 rows: split
+// 6.4, not split 4.5, 128 rows 4.9.
 struct Choice {
   int variant;        // 0 decode, 1 BN = 128, 2 BN = 256, 3 few rows
   unsigned clusters;  // decode: CTAs that share a unit's K
@@ -1397,7 +1398,7 @@ Choice choose(const Args& a, bool gate_up) {
     return (double)((units + sms - 1) / sms) * ((double)kbs * per_kb + end);
   };
   Choice c{0, 1};
-  const double dec = gate_up ? (rows <= 16 ? 0.70 : 0.74) : (rows <= 16 ? 0.36 : 0.42);
+  const double dec = gate_up ? (rows <= 16 ? 0.70 : 0.74) : (rows <= 16 ? 0.33 : 0.36);
   double best = cost(tiles(kNt) * NB, KB, dec, 1.0);
   if (!gate_up) {
     // every cluster has one unit at most, all can run at once, and each CTA has
@@ -1405,20 +1406,20 @@ Choice choose(const Args& a, bool gate_up) {
     const int64_t most = max_tiles(a, kNt) * NB;
     for (unsigned k = 2; k <= 8 && most * k <= sms && KB >= k && most <= max_clusters(k); k *= 2) {
       const double t =
-          cost(most * k, (KB + k - 1) / k, dec, 2.7 + 0.06 * (double)(rows < kNt ? rows : kNt));
+          cost(most * k, (KB + k - 1) / k, dec, 2.4 + 0.08 * (double)(rows < kNt ? rows : kNt));
       if (t < best) {
         best = t;
         c.clusters = k;
       }
     }
-    const double t = cost(tiles(BM) * NB, KB, 0.55, 1.2);
+    const double t = cost(tiles(BM) * NB, KB, 0.45, 1.2);
     if (t < best) {
       best = t;
       c.variant = 1;
     }
   }
   const double t = gate_up ? cost(tiles(BM) * NB, KB, 0.74, 2.5)
-                           : cost(tiles(BM) * ((a.N + 255) / 256), KB, 0.74, 2.0);
+                           : cost(tiles(BM) * ((a.N + 255) / 256), KB, 0.72, 2.0);
   if (t < best) {
     best = t;
     c.variant = 2;
@@ -1426,7 +1427,7 @@ Choice choose(const Args& a, bool gate_up) {
   if (!gate_up && !a.offsets && a.S <= kFewRows && few_smem(a.S, a.K) <= kFewMaxSmem) {
     const int64_t per_wave = (int64_t)sms * kFewWarps;
     const double few = (double)((a.N + per_wave - 1) / per_wave) * ((a.K + 511) / 512) *
-                           (0.12 + 0.14 * (double)a.S) - 1.1;
+                           (0.12 + 0.14 * (double)a.S);
     if (few < best) c.variant = 3;
   }
   return c;
