@@ -690,7 +690,7 @@ int moe_dispatch_fp8(const int32_t* topk_idx, int64_t N, int K, int E, const moe
   const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(x_e);
   if (launch_dispatch(topk_idx, N, K, E, x, d_e, counts, offsets, perm, pos, nullptr,
                       reinterpret_cast<int32_t*>(body_of(ws)), status_of(ws), s,
-                      true) != cudaSuccess ||
+                      true, true) != cudaSuccess ||
       launch_quantize_rows(x, N, d_e, pow2_scales != 0, xq, x_scale, pos, K, N * K, s) !=
           cudaSuccess)
     return MOE_ERR_CUDA;
@@ -868,7 +868,7 @@ int moe_forward_fp8(const moe_bf16* x_r, const moe_bf16* x_e, int64_t N, int d_r
     const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(x_e);
     if (launch_dispatch(idx, N, K, E, x, d_e, reinterpret_cast<int32_t*>(base + L.counts),
                         offsets, reinterpret_cast<int32_t*>(base + L.perm), pos, nullptr,
-                        reinterpret_cast<int32_t*>(stage), st, s) != cudaSuccess ||
+                        reinterpret_cast<int32_t*>(stage), st, s, false, true) != cudaSuccess ||
         launch_quantize_rows(x, N, d_e, pow2_scales != 0, xq, xs, pos, K, N * K, s) !=
             cudaSuccess)
       return MOE_ERR_CUDA;

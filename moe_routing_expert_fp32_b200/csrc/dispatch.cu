@@ -14,9 +14,9 @@
 //   k_scatter one warp per chunk again: every block takes the exclusive scan
 //             of counts (block 0 stores it as offsets), then the slots are
 //             ranked in slot order within the chunk -> pos[slot], perm[pos].
-// Small sorts (at most 4096 slots, at most 1024 experts: decode batches) run
-// the same three passes in one block instead: k_sort_small, 32 warps, warp w
-// the w-th of 32 contiguous chunks, its counts in shared memory.
+// Sorts of at most 65536 slots and 1024 experts run the same three passes in one
+// launch instead: k_sort, one block or a cluster of them, 32 warps each, warp w the
+// w-th of their contiguous chunks, its counts in shared memory.
 // Then k_gather copies every token row once from HBM and writes it to its K
 // sorted positions (token-major, so x_e is read once, not K times).  Without
 // xs (the expert MLP gathering its rows itself) k_gather is skipped.
@@ -206,71 +206,123 @@ __global__ void __launch_bounds__(32 * kWarps) k_scatter(const int32_t* __restri
   }
 }
 
-// The stable counting sort of k_hist + k_scan + k_scatter in one block of 32
-// warps for S <= kSmallSortMaxS slots and E <= kSmallSortMaxE experts: warp w
-// takes the w-th of 32 contiguous chunks of slots, counts them per expert
-// (pass 1), every expert's thread turns the warps' counts into their
-// exclusive prefix and the expert totals into offsets (pass 2), and each warp
-// ranks its slots in slot order (pass 3).  The ranks are those of the
-// three-kernel sort: pos and perm are unique for a stable sort.  The counts
-// are 16-bit (at most 4096 slots), 32 x E of them in dynamic shared memory.
-constexpr int kSmallSortMaxS = 4096;
-constexpr int kSmallSortMaxE = 1024;
-constexpr int kSmallSortRounds = kSmallSortMaxS / (32 * 32);  // slots per lane
+// The stable counting sort of k_hist + k_scan + k_scatter in one launch, of one
+// block (CTAS = 1) or one cluster of CTAS blocks, each of 32 warps, for at most
+// CTAS * 1024 * ROUNDS slots and kSortMaxE experts.  The slots are cut into
+// CTAS * 32 contiguous chunks, one per warp.
+//   1  each warp counts its slots per expert; a slot's rank among its warp's
+//      slots of its expert stays in a register;
+//   2  thread e, expert e: the warps' exclusive prefix and the block's total;
+//      every block reads the others' totals through distributed shared memory and
+//      scans the sums over the experts, which gives the offsets and the place of
+//      its own slots;
+//   3  a slot's position is base[e] + prefix(warp, e) + rank.
+// The ranks are those of the three-kernel sort: pos and perm are unique for a
+// stable sort.  Counts within a block are 16-bit (at most 4096 slots), 32 x E of
+// them in dynamic shared memory.  Bound by latency.
+//
+// A dispatch of rows of 128 columns with 384 experts, measured on a B200 (one
+// block | 8 | 16 | the three kernels, us): 1024 slots 6.2 | 6.3 | - | 14, 2048
+// 7.9 | 6.1 | 6.5 | 14, 4096 11.5 | 7.0 | 6.8 | 14, 16384 - | 9.6 | 8.5 | 14, 32768
+// - | 12.9 | 10.2 | 15, 65536 - | 21 | 14 | 18; with 1024 experts 8192 slots - |
+// 9.3 | 10.2 | 14.
+constexpr int kSortMaxE = 1024;
+constexpr int64_t kSortOneMaxS = 1024;  // <1, 1>
+constexpr int64_t kSortMidMaxS = 8192;  // <8, 1>
+constexpr int64_t kSortMaxS = 65536;    // <16, 4>
+// Callers whose number of launches is documented take the three kernels above this.
+constexpr int64_t kSortThreeMinS = 4096;
 
-__global__ void __launch_bounds__(1024) k_sort_small(const int32_t* __restrict__ idx, int S, int E,
-                                                     int32_t* __restrict__ counts,
-                                                     int32_t* __restrict__ offsets,
-                                                     int32_t* __restrict__ perm,
-                                                     int32_t* __restrict__ pos,
-                                                     DeviceStatus* st, int reset) {
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+size_t sort_smem(int E) {  // total, base, counts
+  return 2 * align_up(sizeof(int32_t) * (size_t)E, 16) + sizeof(int16_t) * 32 * (size_t)E;
+}
+
+template <int CTAS, int ROUNDS>
+__global__ void __launch_bounds__(1024) k_sort(const int32_t* __restrict__ idx, int S, int E,
+                                               int32_t* __restrict__ counts,
+                                               int32_t* __restrict__ offsets,
+                                               int32_t* __restrict__ perm,
+                                               int32_t* __restrict__ pos, DeviceStatus* st,
+                                               int reset) {
   pdl_wait();
   pdl_trigger();
-  if (reset) {  // the first kernel of its call clears the status word
-    if (threadIdx.x == 0) *st = DeviceStatus{0, 0};
-    __syncthreads();
-  }
-  extern __shared__ int16_t cnt_raw[];  // [32][E]
+  extern __shared__ __align__(16) int32_t total[];  // [E] of this block, read by the others
+  const int E4 = (E + 3) & ~3;
+  int32_t* base = total + E4;                                // [E] of this block's slots
+  int16_t* cnt_raw = reinterpret_cast<int16_t*>(base + E4);  // [32][E]
   __shared__ int32_t warp_tot[32];
   auto cnt = [&](int w, int e) -> int16_t& { return cnt_raw[w * E + e]; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int CH = (S + 31) / 32;
-  const int beg = warp * CH;
+  const int rank = CTAS > 1 ? blockIdx.x : 0;  // the grid is one cluster
+  // the first kernel of its call clears the status word
+  if (reset && rank == 0 && threadIdx.x == 0) *st = DeviceStatus{0, 0};
+  const int CH = (S + 32 * CTAS - 1) / (32 * CTAS);
+  const int beg = (rank * 32 + warp) * CH;
   const int end = beg + CH < S ? beg + CH : S;
-  for (int e = lane; e < E; e += 32) cnt(warp, e) = 0;
-  __syncwarp();
-  // pass 1: this warp's counts; the slot indices stay in registers
-  int ev[kSmallSortRounds];
+  int ev[ROUNDS], rk[ROUNDS];
+  bool bad = false;
 #pragma unroll
-  for (int i = 0; i < kSmallSortRounds; ++i) {
+  for (int i = 0; i < ROUNDS; ++i) {
     const int slot = beg + 32 * i + lane;
-    int e = slot < end ? idx[slot] : -1;
-    if (slot < end && (e < 0 || e >= E)) {
-      record_error(st, MOE_ERR_DEVICE_BOUNDS, 10);
-      e = -1;
-    }
-    ev[i] = e;
+    ev[i] = slot < end ? idx[slot] : -1;
   }
+  for (int i = threadIdx.x; i < 4 * E; i += 1024)  // 64 * E bytes
+    reinterpret_cast<uint4*>(cnt_raw)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  const unsigned lt = lanemask_lt();
 #pragma unroll
-  for (int i = 0; i < kSmallSortRounds; ++i) {
-    const unsigned peers = __match_any_sync(0xffffffffu, ev[i]);
-    if (ev[i] >= 0 && lane == __ffs(peers) - 1)
-      cnt(warp, ev[i]) = (int16_t)(cnt(warp, ev[i]) + __popc(peers));
-    __syncwarp();
+  for (int i = 0; i < ROUNDS; ++i) {
+    if (beg + 32 * i + lane < end && (ev[i] < 0 || ev[i] >= E)) {
+      bad = true;
+      ev[i] = -1;
+    }
+    if (32 * i < CH) {
+      const unsigned peers = __match_any_sync(0xffffffffu, ev[i]);
+      const int32_t had = ev[i] >= 0 ? cnt(warp, ev[i]) : 0;
+      rk[i] = had + __popc(peers & lt);
+      __syncwarp();
+      if (ev[i] >= 0 && lane == __ffs(peers) - 1)
+        cnt(warp, ev[i]) = (int16_t)(had + __popc(peers));
+      __syncwarp();
+    }
   }
   __syncthreads();
-  // pass 2: thread e, expert e: the warps' exclusive prefix, the total, then
-  // the exclusive scan of the totals over the experts
   const int e = threadIdx.x;
-  int32_t tot = 0;
+  int32_t before = 0, tot = 0;
   if (e < E) {
-    for (int w = 0; w < 32; ++w) {
-      const int32_t t = cnt(w, e);
-      cnt(w, e) = (int16_t)tot;
-      tot += t;
+    for (int w = 0; w < 32; w += 8) {
+      int32_t t[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = cnt(w + j, e);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        cnt(w + j, e) = (int16_t)tot;
+        tot += t[j];
+      }
     }
-    counts[e] = tot;
+    if (CTAS > 1) total[e] = tot;
   }
+  if (CTAS > 1) {
+    cluster_barrier();  // the totals of all blocks are there
+    if (e < E) {
+      const uint32_t mine = (uint32_t)__cvta_generic_to_shared(total + e);
+      tot = 0;
+#pragma unroll
+      for (int r = 0; r < CTAS; ++r) {
+        uint32_t at;
+        int32_t t;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(mine), "r"(r));
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(t) : "r"(at) : "memory");
+        if (r < rank) before += t;
+        tot += t;
+      }
+    }
+  }
+  if (bad) record_error(st, MOE_ERR_DEVICE_BOUNDS, 10);  // behind a barrier after the reset
   int32_t v = tot;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -282,32 +334,107 @@ __global__ void __launch_bounds__(1024) k_sort_small(const int32_t* __restrict__
   int32_t off = v - tot;
   for (int i = 0; i < warp; ++i) off += warp_tot[i];
   if (e < E) {
-    offsets[e] = off;
-    for (int w = 0; w < 32; ++w) cnt(w, e) = (int16_t)(cnt(w, e) + off);
-    if (e == E - 1) offsets[E] = off + tot;
-  }
-  __syncthreads();
-  // pass 3: ranks in slot order, as k_scatter
-  const unsigned lt = lanemask_lt();
-#pragma unroll
-  for (int i = 0; i < kSmallSortRounds; ++i) {
-    const int slot = beg + 32 * i + lane;
-    const int ee = ev[i];
-    const unsigned peers = __match_any_sync(0xffffffffu, ee);
-    if (slot < end) {
-      if (ee >= 0) {
-        const int32_t p = cnt(warp, ee) + __popc(peers & lt);
-        pos[slot] = p;
-        perm[p] = slot;
-      } else {
-        pos[slot] = -1;
-      }
+    base[e] = off + before;
+    if (rank == 0) {
+      counts[e] = tot;
+      offsets[e] = off;
+      if (e == E - 1) offsets[E] = off + tot;
     }
-    __syncwarp();
-    if (ee >= 0 && lane == __ffs(peers) - 1)
-      cnt(warp, ee) = (int16_t)(cnt(warp, ee) + __popc(peers));
-    __syncwarp();
   }
+  // base is written; no block of a cluster leaves before all have read its totals
+  if (CTAS > 1)
+    cluster_barrier();
+  else
+    __syncthreads();
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) {
+    const int slot = beg + 32 * i + lane;
+    if (slot < end) {
+      int32_t p = -1;
+      if (ev[i] >= 0) {
+        p = base[ev[i]] + cnt(warp, ev[i]) + rk[i];
+        perm[p] = slot;
+      }
+      pos[slot] = p;
+    }
+  }
+}
+
+cudaLaunchConfig_t sort_config(int ctas, int E, cudaStream_t s, cudaLaunchAttribute* attr) {
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(1024);
+  cfg.dynamicSmemBytes = sort_smem(E);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  return cfg;
+}
+
+// *runs: whether the device can run the cluster at all (16 blocks are more than
+// every device promises)
+template <int CTAS, int ROUNDS>
+cudaError_t set_up_sort(bool* runs) {
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t set_up[kMaxDevices];
+  static bool fits[kMaxDevices];
+  const cudaError_t e = once_per_device(once, set_up, [](int dev) {
+    constexpr auto kernel = k_sort<CTAS, ROUNDS>;
+    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sort_smem(kSortMaxE));
+    if (CTAS > 8 && r == cudaSuccess)
+      r = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    int most = 1;
+    if (CTAS > 1 && r == cudaSuccess) {
+      cudaLaunchAttribute attr[2];
+      cudaLaunchConfig_t cfg = sort_config(CTAS, kSortMaxE, nullptr, attr);
+      cfg.attrs = attr + 1;
+      cfg.numAttrs = 1;
+      r = cudaOccupancyMaxActiveClusters(&most, kernel, &cfg);
+    }
+    fits[dev] = most > 0;
+    return r;
+  });
+  int dev = 0;
+  if (e != cudaSuccess) return e;
+  const cudaError_t d = cudaGetDevice(&dev);
+  *runs = d == cudaSuccess && fits[dev];
+  return d;
+}
+
+struct SortArgs {
+  const int32_t* idx;
+  int S, E;
+  int32_t *counts, *offsets, *perm, *pos;
+  DeviceStatus* st;
+  bool reset;
+};
+
+template <int CTAS, int ROUNDS>
+cudaError_t launch_sort(const SortArgs& a, cudaStream_t s) {
+  static_assert(1024 * ROUNDS <= INT16_MAX, "a block's counts are 16-bit");
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = sort_config(CTAS, a.E, s, attr);
+  return counted(cudaLaunchKernelEx(&cfg, k_sort<CTAS, ROUNDS>, a.idx, a.S, a.E, a.counts,
+                                    a.offsets, a.perm, a.pos, a.st, a.reset ? 1 : 0));
+}
+
+// The one-launch sort where it applies: *done says whether it was launched.
+cudaError_t one_launch_sort(const SortArgs& a, int64_t S, cudaStream_t s, bool* done) {
+  *done = false;
+  if (S < 1 || S > kSortMaxS || a.E > kSortMaxE) return cudaSuccess;
+  cudaError_t e = S <= kSortOneMaxS   ? set_up_sort<1, 1>(done)
+                  : S <= kSortMidMaxS ? set_up_sort<8, 1>(done)
+                                      : set_up_sort<16, 4>(done);
+  if (e != cudaSuccess || !*done) return e;
+  return S <= kSortOneMaxS   ? launch_sort<1, 1>(a, s)
+         : S <= kSortMidMaxS ? launch_sort<8, 1>(a, s)
+                             : launch_sort<16, 4>(a, s);
 }
 
 // One warp per (token, chunk of 256 columns): each lane reads one 16-byte
@@ -422,22 +549,15 @@ size_t dispatch_scratch_bytes(int64_t S, int E) {
 cudaError_t launch_dispatch(const int32_t* idx, int64_t N, int K, int E, const __nv_bfloat16* x_e,
                             int d_e, int32_t* counts, int32_t* offsets, int32_t* perm,
                             int32_t* pos, __nv_bfloat16* xs, int32_t* scratch, DeviceStatus* st,
-                            cudaStream_t s, bool reset) {
+                            cudaStream_t s, bool reset, bool one_launch) {
   const int64_t S = N * K;
   cudaError_t e;
-  if (S >= 1 && S <= kSmallSortMaxS && E <= kSmallSortMaxE) {
-    static std::once_flag once[kMaxDevices];
-    static cudaError_t set_up[kMaxDevices];
-    if ((e = once_per_device(once, set_up, [](int) {
-           return cudaFuncSetAttribute(k_sort_small, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(sizeof(int16_t) * 32 * kSmallSortMaxE));
-         })) != cudaSuccess)
-      return e;
-    const size_t smem = sizeof(int16_t) * 32 * (size_t)E;
-    if ((e = launch_pdl(k_sort_small, dim3(1), dim3(1024), smem, s, idx, (int)S, E, counts,
-                        offsets, perm, pos, st, reset ? 1 : 0)) != cudaSuccess)
-      return e;
-  } else {
+  bool sorted = false;
+  const SortArgs sort{idx, (int)S, E, counts, offsets, perm, pos, st, reset};
+  if ((one_launch || S <= kSortThreeMinS) &&
+      (e = one_launch_sort(sort, S, s, &sorted)) != cudaSuccess)
+    return e;
+  if (!sorted) {
     if (reset && (e = cudaMemsetAsync(st, 0, sizeof(DeviceStatus), s)) != cudaSuccess) return e;
     const int CH = dispatch_chunk_len(S);
     const int nchunks = dispatch_chunks(S);

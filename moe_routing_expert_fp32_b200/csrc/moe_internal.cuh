@@ -113,11 +113,12 @@ cudaError_t launch_select(const float* logits, int64_t N, const float* bias,
 int dispatch_chunks(int64_t S);
 size_t dispatch_scratch_bytes(int64_t S, int E);
 // xs == nullptr: counts, offsets, perm and pos only (no gather);
-// reset: clear the status word first (else the caller has)
+// reset: clear the status word first (else the caller has);
+// one_launch: sort in one launch above 4096 slots too, where it is faster
 cudaError_t launch_dispatch(const int32_t* idx, int64_t N, int K, int E, const __nv_bfloat16* x_e,
                             int d_e, int32_t* counts, int32_t* offsets, int32_t* perm,
                             int32_t* pos, __nv_bfloat16* xs, int32_t* scratch, DeviceStatus* st,
-                            cudaStream_t s, bool reset = false);
+                            cudaStream_t s, bool reset = false, bool one_launch = false);
 
 // offsets [n+1] = exclusive prefix of counts [n] (n <= 1024)
 cudaError_t launch_counts_offsets(const int32_t* counts, int n, int32_t* offsets,

@@ -97,6 +97,38 @@ def test_dispatch_fp8(moe, N, K, E, d, pow2):
     assert torch.equal(xq.float(), qr[0][tok]) and torch.equal(xs, sr[0][tok])
 
 
+@pytest.mark.parametrize("E", [1, 37, 256, 1000, 1024])
+@pytest.mark.parametrize("N,K", [(1, 1), (31, 1), (1024, 1), (1025, 1), (341, 7), (1024, 8),
+                                 (2731, 3), (8192, 2), (4681, 14), (8192, 8), (65537, 1)])
+def test_dispatch_fp8_sort(moe, N, K, E):
+    """The sort behind the dispatch is the stable one, around the sizes where it
+    changes its form, with skewed and with bad indices, and as often as it runs."""
+    g = gen(N + K + E)
+    idx = (torch.rand(N, K, generator=g, device="cuda") ** 3 * E).to(torch.int32).clamp(max=E - 1)
+    if E > 1:
+        idx[N // 2:, 0] = 1  # a long run of one expert
+    bad = torch.rand(N, K, generator=g, device="cuda") < 0.02
+    x = torch.randn(N, 16, generator=g, device="cuda").to(torch.bfloat16)
+    xq0, xs0 = moe.quantize_fp8(x)
+    ws = moe.workspace(moe.lib().moe_dispatch_workspace_size(N, K, E))
+    for i in (idx, torch.where(bad, torch.full_like(idx, E), idx),
+              torch.full_like(idx, E - 1), idx):
+        flat = i.reshape(-1).long()
+        live = (flat < E).nonzero().squeeze(1)
+        order = live[torch.sort(flat[live], stable=True).indices]
+        n = torch.bincount(flat[live], minlength=E)
+        p_ref = torch.full_like(flat, -1)
+        p_ref[order] = torch.arange(len(order), device="cuda")
+        counts, offsets, perm, pos, xq, xs = moe.dispatch_fp8(i, x, E, ws=ws)
+        assert moe.get_status(ws) == (-7 if len(live) < N * K else 0)
+        assert torch.equal(counts.long(), n)
+        assert torch.equal(offsets[1:].long(), n.cumsum(0)) and int(offsets[0]) == 0
+        assert torch.equal(perm[:len(order)].long(), order)
+        assert torch.equal(pos.long(), p_ref)
+        assert torch.equal(bits(xq[:len(order)]), bits(xq0[order // K]))
+        assert torch.equal(xs[:len(order)], xs0[order // K])
+
+
 def test_dispatch_fp8_leaves_out_bad_indices(moe):
     """A slot with an expert outside [0, E) is recorded and left out; rows behind
     the last kept slot stay as they were."""
