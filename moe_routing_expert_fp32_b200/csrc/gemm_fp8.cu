@@ -530,6 +530,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       fetch(0);
+      // plain: kOutCols columns of y, and of the residual before them, pass through the
+      // warp's shared memory, a row's 16-byte words permuted against bank conflicts.
+      // The residual's first columns are copied while the K blocks run, the next ones
+      // after each store, from L2 (4096 rows, 2048 to 7168: 143 us when each lane
+      // loaded them there, 105 so, 88 without a residual; held in registers instead,
+      // the sums spill: 133).
+      constexpr int kW = C::kOutCols / 8;  // 16-byte words per row
+      constexpr int kRowsAt = 32 / kW;     // rows per warp-wide access
+      uint8_t* ob = out_x + warp * C::kOutBytes;
+      auto word = [&](int r, int j) {
+        return reinterpret_cast<uint4*>(ob + r * (16 * kW) + 16 * (j ^ ((r >> 1) & 3)));
+      };
+      auto res_async = [&](int c) {  // of columns c .. c + kOutCols - 1
+        const int n = c + 8 * (lane % kW);
+        const __nv_bfloat16* p = a.res + row0 * a.N + w.nb * BN + NC * half + n;
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+          const int r = i * kRowsAt + lane / kW;
+          if (n < cols && r < rows)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             smem_u32(word(r, lane % kW))),
+                         "l"(p + (int64_t)r * a.N)
+                         : "memory");
+        }
+      };
+      if (MODE == kPlain && a.res) {
+        // the residual of the first columns to shared memory, of the others into L2
+        res_async(0);
+        const __nv_bfloat16* p = a.res + row0 * a.N + w.nb * BN + NC * half;
+#pragma unroll
+        for (int c = C::kOutCols; c < NC; c += C::kOutCols)
+          if (live && c < cols)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p + (int64_t)lane * a.N + c));
+      }
       uint64_t acc2[NC / 2];  // the sums of columns 2i and 2i + 1
 #pragma unroll
       for (int i = 0; i < NC / 2; ++i) acc2[i] = 0;
@@ -577,29 +611,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if constexpr (MODE == kPlain) {
-        // kOutCols columns at a time through shared memory, so that a store
-        // covers whole sectors of few rows (each lane's own row, 16 bytes at a
-        // time, took 6,000 cycles a unit); a row's 16-byte words are permuted
-        // against bank conflicts.  The residual comes the same way.
-        constexpr int kW = C::kOutCols / 8;  // 16-byte words per row
-        constexpr int kRowsAt = 32 / kW;     // rows per warp-wide access
-        uint8_t* ob = out_x + warp * C::kOutBytes;
-        auto word = [&](int r, int j) {
-          return reinterpret_cast<uint4*>(ob + r * (16 * kW) + 16 * (j ^ ((r >> 1) & 3)));
-        };
+        // Through shared memory a store covers whole sectors of few rows (each
+        // lane's own row, 16 bytes at a time, took 6,000 cycles a unit).
         const int n_first = w.nb * BN + NC * half;
 #pragma unroll
         for (int c = 0; c < NC; c += C::kOutCols) {
           const int n = n_first + c + 8 * (lane % kW);  // of this lane's accesses to y
           const bool in = n < a.N;                      // N is a multiple of 8
           if (a.res) {
-#pragma unroll
-            for (int i = 0; i < kW; ++i) {
-              const int r = i * kRowsAt + lane / kW;
-              if (in && r < rows)
-                *word(r, lane % kW) =
-                    *reinterpret_cast<const uint4*>(a.res + (row0 + r) * a.N + n);
-            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
           }
 #pragma unroll
@@ -635,6 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint4*>(a.y + (row0 + r) * a.N + n) = *word(r, lane % kW);
           }
           __syncwarp();
+          if (a.res && c + C::kOutCols < NC) res_async(c + C::kOutCols);
         }
       } else {
         float acc[NC];
@@ -668,11 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float inv;
         const float s = fp8::block_scale(__uint_as_float(m), a.pow2, inv);
         // the warp's 32 x 64 bytes through shared memory, as in the plain form
-        uint8_t* ob = out_x + warp * C::kOutBytes;
-        static_assert(C::kOutBytes == 32 * 64, "32 rows of 64 bytes");
-        auto word = [&](int r, int j) {
-          return reinterpret_cast<uint4*>(ob + r * 64 + 16 * (j ^ ((r >> 1) & 3)));
-        };
+        static_assert(C::kOutBytes == 32 * 64 && kW == 4, "32 rows of 64 bytes");
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t o[4];
@@ -695,6 +712,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
+    // a unit that was given up may have left copies of the residual in flight
+    if (MODE == kPlain) asm volatile("cp.async.wait_all;" ::: "memory");
   }  // roles
   tc_fence_before();
   __syncthreads();
