@@ -475,7 +475,8 @@ MOE_API int moe_block_forward(const moe_bf16* x, int64_t N, const moe_block_dims
  * moe_quantize_fp8 gives.  Products are summed in fp32: 128 columns of K in the
  * tensor core, times the product of the two scales (itself rounded to fp32),
  * then over the blocks in order; one rounding to bf16 at the end.  A call's
- * results depend on its arguments alone, bit for bit. */
+ * results depend on its arguments alone, bit for bit.  Outputs and workspace
+ * overlap neither each other nor an operand, but for moe_linear_fp8's y. */
 typedef uint8_t moe_fp8; /* e4m3 bit pattern (no infinities, NaN 0x7f) */
 
 /* bf16 to the 8-bit format.  x [B, M, K] bf16; q [B, M, K] e4m3.
@@ -501,7 +502,8 @@ MOE_API int moe_dispatch_fp8(const int32_t* topk_idx, int64_t N, int K, int E,
 
 /* moe_linear on 8-bit operands: y[m, n] = bf16( sum_k x[m, k] * W[n, k]
  * (+ residual[m, n]) ), rounded once.  xq [M, K], w [N_out, K]; residual
- * (may be NULL) and y [M, N_out] bf16.  y may be the residual buffer. */
+ * (may be NULL) and y [M, N_out] bf16.  y may be the residual buffer (the same
+ * pointer, not a shifted one). */
 MOE_API size_t moe_linear_fp8_workspace_size(int64_t M, int K, int N_out);
 MOE_API int moe_linear_fp8(const moe_fp8* xq, const float* x_scale, int64_t M, int K,
                            const moe_fp8* w, const float* w_scale, int N_out,

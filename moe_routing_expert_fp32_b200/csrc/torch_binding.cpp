@@ -178,7 +178,14 @@ float float_of(PyObject* o, const char* name) {
   }
   return (float)v;
 }
-bool flag_of(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool flag_of(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    throw Refusal{std::string(name) + " must be true or false"};
+  }
+  return v == 1;
+}
 
 int64_t c128(int64_t n) { return (n + 127) / 128; }
 template <typename T = void>
@@ -194,7 +201,7 @@ PyObject* quantize(PyObject* const* a) {
   Tensors ts;
   const at::Tensor& x = ts.any(a[0], "x", at::kBFloat16);
   const int rows = int32_of(a[1], "block_rows");
-  const bool pow2 = flag_of(a[2]);
+  const bool pow2 = flag_of(a[2], "pow2_scales");
   const int64_t n = x.dim();
   if (rows == 1 ? n < 1 : n != 2 && n != 3)
     throw Refusal{rows == 1 ? "x needs at least one dimension"
@@ -229,8 +236,9 @@ PyObject* dispatch(PyObject* const* a) {
   if (x.size(0) != N)
     throw Refusal{"x_e has shape " + text_of(x.sizes()) + ", expected " + text_of({N, d})};
   const int E = int32_of(a[2], "num_experts");
-  const bool pow2 = flag_of(a[3]);
+  const bool pow2 = flag_of(a[3], "pow2_scales");
   if (E < 1) throw Refusal{"num_experts must be positive"};
+  if (E > 1024) return PyLong_FromLong(MOE_ERR_UNSUPPORTED);  // before allocating for it
   // the integers and, without a caller's workspace, the workspace share an
   // allocation
   const size_t need = a[4] == Py_None ? moe_dispatch_workspace_size(N, K, E) : 0;
@@ -338,7 +346,7 @@ PyObject* expert_ffn(PyObject* const* a) {
   const at::Tensor& xs = ts.get(a[1], "x_scale", at::kFloat, {S, c128(d)});
   const at::Tensor& off = ts.get(a[2], "offsets", at::kInt, {(int64_t)E + 1});
   const moe_act_cfg act = act_of(a + 9);
-  const bool pow2 = flag_of(a[12]);
+  const bool pow2 = flag_of(a[12], "pow2_scales");
   const at::Tensor y = ts.out(a[13], "y", at::kBFloat16, {S, d});
   const Workspace wk =
       workspace(ts, a[14], a[14] == Py_None ? moe_expert_ffn_fp8_workspace_size(S, d, E, F) : 0);
@@ -362,7 +370,7 @@ PyObject* forward(PyObject* const* a) {
   c.n_group = int32_of(r[1], "n_group");
   c.topk_group = int32_of(r[2], "topk_group");
   c.top_k = int32_of(r[3], "top_k");
-  c.norm_topk_prob = flag_of(r[4]);
+  c.norm_topk_prob = flag_of(r[4], "norm_topk_prob");
   c.route_scale = float_of(r[5], "route_scale");
   c.score_func = int32_of(r[6], "score_func");
   c.group_score = int32_of(r[7], "group_score");
@@ -377,7 +385,7 @@ PyObject* forward(PyObject* const* a) {
     throw Refusal{"x_e is required when the experts' width differs from the router's"};
   const moe_bf16* x_e =
       a[9] == Py_None ? nullptr : bf(ts.get(a[9], "x_e", at::kBFloat16, {N, d}));
-  const bool pow2 = flag_of(a[10]);
+  const bool pow2 = flag_of(a[10], "pow2_scales");
   const Workspace wk = workspace(
       ts, a[11], a[11] == Py_None ? moe_forward_fp8_workspace_size(N, d_r, d, &c, F) : 0);
   const at::Tensor out = ts.out(a[12], "out", at::kBFloat16, {N, d});

@@ -529,3 +529,17 @@ def test_wait_probe_stops_the_8_bit_kernels(moe, counts):
     assert (y == 2.0).all()
     moe.expert_ffn_fp8(xq, xs, off, *w, moe.ActConfig("silu"), y=y, ws=wk)
     assert moe.get_status(wk) == 0 and torch.equal(bits(y), bits(good))
+
+
+def test_refusals_of_arguments(moe):
+    """A flag that has no truth value, and more experts than the sort takes (before
+    anything is allocated for them)."""
+    x = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
+    idx = torch.zeros(4, 1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="pow2_scales"):
+        moe.quantize_fp8(x, pow2_scales=torch.ones(2))
+    with pytest.raises(ValueError, match="pow2_scales"):
+        moe.dispatch_fp8(idx, x, 8, pow2_scales=torch.ones(2))
+    for E in (1025, 2 ** 31 - 1):
+        with pytest.raises(moe.MoeError):
+            moe.dispatch_fp8(idx, x, E)
