@@ -77,8 +77,9 @@ def product(xq, xs, w, ws, res=None):
 
 
 # Relative error of the activations' fp32 functions: exp, reciprocal and tanh
-# each within a few fp32 steps; 1 - 2/(e^2x + 1) from |x| = 0.25 on cancels to a
-# quarter, so 8e-7 there; the argument of exp carries |g| u.
+# each within a few fp32 steps; e^2x - 1 is used from |x| = 0.125 on, where it is
+# 0.22 of e^2x, so e^2x's 2^-22 becomes 1.1e-6 there, twice with two tanh; the
+# argument of exp carries |g| u.
 ACT_REL = 2.0 ** -18
 
 
@@ -103,7 +104,7 @@ def ffn(xq, xs, w1, w1s, w3, w3s, w2, w2s, kind, beta, lbeta, pow2):
     g, u = x @ W1.t(), x @ W3.t()
     eg, eu = c * (x.abs() @ W1.abs().t()), c * (x.abs() @ W3.abs().t())
     h = act64(g, u, kind, beta, lbeta)
-    slope = 1.1 if kind == "silu" else 1.0 + beta / 4
+    slope = 1.1 if kind == "silu" else 1.0 + abs(beta) / 4
     left = act64(g, torch.ones_like(u), kind, beta, 0.0).abs()
     umag = u.abs() if kind == "silu" or not lbeta else (lbeta * torch.tanh(u / lbeta)).abs()
     eh = slope * eg * (umag + eu) + left * eu + ACT_REL * h.abs()

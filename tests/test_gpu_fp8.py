@@ -347,6 +347,26 @@ def test_expert_ffn_fp8_large_gates(moe):
             R.assert_within(y[a:b], ref, bound, f"{act} expert {e}")
 
 
+@pytest.mark.parametrize("counts", [[20, 9], [300, 200]])
+@pytest.mark.parametrize("act,beta,lbeta", [("silu", 1.0, 0.0), ("situ", 4.0, 8.0),
+                                            ("situ", 2.0, 0.0), ("situ", -1.0, 0.5)])
+def test_expert_ffn_fp8_argument_sizes(moe, act, beta, lbeta, counts):
+    """The activation from arguments where tanh is its argument, over the border of
+    its series, to where it is 1, in the kernels of few and of many rows."""
+    off, S = offsets_of(counts)
+    g = gen(21)
+    xq, xs, w = make_ffn(g, 2, 256, 256, S, False)
+    for by in (1e-5, 0.01, 0.08, 0.5, 8.0):
+        v = (w[0], w[1] * by, w[2], w[3] * by, *w[4:])
+        y = moe.expert_ffn_fp8(xq, xs, off, *v, moe.ActConfig(act, beta, lbeta))
+        a = 0
+        for e, n in enumerate(counts):
+            ref, bound = R.ffn(xq[a:a + n], xs[a:a + n], *[t[e] for t in v], act, beta, lbeta,
+                               False)
+            R.assert_within(y[a:a + n], ref, bound, f"x {by}, expert {e}")
+            a += n
+
+
 # ---------------------------------------------------------- the run together
 def layer_inputs(moe, N=100, d_r=256, d_e=256, E=16, F=128, K=4, seed=3):
     g = gen(seed)
