@@ -364,6 +364,12 @@ __device__ __forceinline__ const int32_t* build_tiles(const Args& a, int tile,
 struct Unit {
   int e, row0, nrows, nb;
 };
+// Fewer than 2^31 for segments that do not overlap.  Behind one that runs backwards
+// others may: what is more of them then is left out.
+__device__ __forceinline__ uint32_t units_of(int tiles, int RB) {
+  const uint64_t n = (uint64_t)tiles * (uint32_t)RB;
+  return n < 0x7fffffffu ? (uint32_t)n : 0x7fffffffu;
+}
 // Unit u: weight block u % RB of token tile u / RB.
 __device__ __forceinline__ Unit unit_at(int E, const int32_t* offsets, const int32_t* tile_start,
                                         int RB, int tile, uint32_t u) {
@@ -444,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t* off = build_tiles<kThreads, C::kCache>(a, BM, tile_start, off_x, warp_tot);
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const uint32_t total_units = (uint32_t)tile_start[a.E] * (uint32_t)RB;  // < 2^31
+  const uint32_t total_units = units_of(tile_start[a.E], RB);
 
   auto unit_of = [&](uint32_t u) { return unit_at(a.E, off, tile_start, RB, BM, u); };
 
@@ -908,7 +914,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   tc_fence_after();
   if (SPLIT) cluster_sync();  // the other CTAs run: their shared memory may be written
   const uint32_t tmem_base = *tmem_slot;
-  const uint32_t total_units = (uint32_t)tile_start[a.E] * (uint32_t)NB;  // < 2^31
+  uint32_t total_units = units_of(tile_start[a.E], NB);
+  if (SPLIT && total_units > unit_step) total_units = unit_step;  // (overlapping segments)
   auto unit_of = [&](uint32_t u) { return unit_at(a.E, off, tile_start, NB, kNt, u); };
 
   if (warp == 4) {
@@ -1535,8 +1542,11 @@ cudaError_t launch_few(const Operands& o, const Args& args, cudaStream_t s) {
 
 template <int MODE>
 int run_product(const Operands& o, const Args& args, cudaStream_t s) {
-  // units are counted in 31 bits (more would be a terabyte of weights or outputs)
-  if (max_tiles(args, kNt) > INT32_MAX / ((args.N + 127) / 128)) return MOE_ERR_UNSUPPORTED;
+  // units are counted in 31 bits (more would be a terabyte of weights or outputs),
+  // tiles too, even where segments behind a bad one overlap
+  if (max_tiles(args, kNt) > INT32_MAX / ((args.N + 127) / 128) ||
+      (args.S / kNt + 1) * args.E > INT32_MAX)
+    return MOE_ERR_UNSUPPORTED;
   const Choice c = choose(args, MODE == kGateUp);
   if (c.variant == 3) {
     const cudaError_t e = args.S == 1   ? launch_few<1>(o, args, s)

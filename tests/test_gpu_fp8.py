@@ -299,6 +299,28 @@ def test_grouped_bad_offsets_are_recorded(moe, bad):
 
 
 # ---------------------------------------------------------------- expert MLP
+@pytest.mark.parametrize("K,N", [(2048, 128), (256, 1024)])
+def test_grouped_fp8_overlapping_segments(moe, K, N):
+    """Segments behind one that runs backwards may overlap, more tiles than rows: the
+    error is recorded, nothing outside the rows is written, and the next call is
+    as always (with K split over a cluster too)."""
+    E, S = 8, 100
+    off = torch.tensor([0, 100] * 4 + [0], dtype=torch.int32, device="cuda")
+    g = gen(31)
+    xq, xs = R.rand_rows(g, S, K)
+    w, ws = R.rand_weights(g, E, N, K)
+    buf = torch.full((S + 64, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    wk = moe.workspace(moe.lib().moe_grouped_linear_fp8_workspace_size(S, K, E, N))
+    moe.grouped_linear_fp8(xq, xs, off, w, ws, out=buf[32:32 + S], ws=wk)
+    assert moe.get_status(wk) == -7
+    assert (buf[:32] == 3).all() and (buf[32 + S:] == 3).all()
+    off = torch.tensor([0] + [100] * 8, dtype=torch.int32, device="cuda")
+    y = moe.grouped_linear_fp8(xq, xs, off, w, ws, ws=wk)
+    assert moe.get_status(wk) == 0
+    ref, bound = R.product(xq, xs, w[0], ws[0])
+    R.assert_within(y, ref, bound)
+
+
 def make_ffn(g, E, d, F, S, pow2):
     xq, xs = R.rand_rows(g, S, d, pow2)
     w1, w1s = R.rand_weights(g, E, F, d)
