@@ -104,23 +104,28 @@ Workspace workspace(Tensors& ts, PyObject* o, size_t need) {
 }
 
 // For calls that need only the status word: without a caller's workspace, one
-// that the calls of a device share (nothing reads its status).
+// that the calls of a device share (nothing reads its status, so it does not
+// matter that calls on several streams clear it).  It comes from cudaMalloc: a
+// block of the caching allocator may still be in use by work queued on the stream
+// that freed it, which a call on another stream does not wait for.
 Workspace status_only(Tensors& ts, PyObject* o) {
   if (o != Py_None) return given(ts, o);
   constexpr int kDevices = 64;
-  static at::Tensor* kept = new at::Tensor[kDevices];  // never freed: outlives the CUDA runtime
-  const bool keep = ts.dev < kDevices;
-  if (keep && kept[ts.dev].defined()) {
-    Workspace w;
-    w.t = kept[ts.dev];
-    w.p = w.t.data_ptr();
-    w.bytes = 256;
-    return w;
+  static void* kept[kDevices] = {};  // never freed
+  if (ts.dev >= kDevices) return workspace(ts, Py_None, 256);
+  if (!kept[ts.dev]) {
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)ts.dev);
+    // an allocation is no part of a graph that this or another thread captures
+    const c10::cuda::CUDAStreamCaptureModeGuard relaxed(cudaStreamCaptureModeRelaxed);
+    if (cudaMalloc(&kept[ts.dev], 256) != cudaSuccess) {
+      (void)cudaGetLastError();  // no memory outside the allocator: one of the call's own
+      kept[ts.dev] = nullptr;
+      return workspace(ts, Py_None, 256);
+    }
   }
-  Workspace w = workspace(ts, Py_None, 256);
-  // (not memory of a graph's pool)
-  if (keep && c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None)
-    kept[ts.dev] = w.t;
+  Workspace w;
+  w.p = kept[ts.dev];
+  w.bytes = 256;
   return w;
 }
 
