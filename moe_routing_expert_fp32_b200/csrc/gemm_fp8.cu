@@ -25,6 +25,7 @@
 #include <cuda.h>
 
 #include <cuda_fp16.h>
+#include <float.h>
 
 #include "fp8.cuh"
 #include "moe_internal.cuh"
@@ -158,8 +159,11 @@ __device__ __forceinline__ Act make_act(int kind, float beta, float lbeta) {
   t.has_lb = !(lbeta == 0.0f || lbeta != lbeta);
   t.beta = (beta == 0.0f || beta != beta) ? 1.0f : beta;
   t.lbeta = lbeta;
-  t.inv_beta = __fdiv_rn(1.0f, t.beta);
-  t.inv_lbeta = t.has_lb ? __fdiv_rn(1.0f, lbeta) : 0.0f;
+  // (finite below 2^-128 too, where 0 times an infinity would make a gate of 0 NaN;
+  // arguments that such a limit does not saturate are subnormal themselves)
+  auto inverse = [](float b) { return fmaxf(-FLT_MAX, fminf(__fdiv_rn(1.0f, b), FLT_MAX)); };
+  t.inv_beta = inverse(t.beta);
+  t.inv_lbeta = t.has_lb ? inverse(lbeta) : 0.0f;
   return t;
 }
 __device__ __forceinline__ float exp2_ftz(float x) {
