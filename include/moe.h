@@ -470,7 +470,9 @@ MOE_API int moe_block_forward(const moe_bf16* x, int64_t N, const moe_block_dims
  *     scale [B, ceil(N/128), ceil(K/128)].
  * Blocks at the ends may be partial.  Limits: K (the contracted width) a
  * multiple of 16, N (an output width) a multiple of 8, both at most 2^30; E at
- * most 1024; e4m3 and bf16 pointers 16-byte aligned, scales 4-byte aligned.
+ * most 1024; of a product's S rows, (S/32 + min(S, E)) * ceil(N/128) and
+ * (S/32 + 1) * E below 2^31; e4m3 and bf16 pointers 16-byte aligned, scales
+ * 4-byte aligned.
  * Scales are the caller's: any fp32 values, not only those that
  * moe_quantize_fp8 gives.  Products are summed in fp32: 128 columns of K in the
  * tensor core, times the product of the two scales (itself rounded to fp32),

@@ -619,11 +619,13 @@ int check_fp8_product(int64_t S, int K, int E, int N) {
   if (S < 0 || K <= 0 || E < 1 || N <= 0) return MOE_ERR_INVALID_ARG;
   if (E > 1024 || K % 16 != 0 || N % 8 != 0 || S > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (K > (1 << 30) || N > (1 << 30)) return MOE_ERR_UNSUPPORTED;  // 32-bit column indexes
-  return MOE_OK;
+  return fp8_units_fit(S, E, N) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
 int check_fp8_ffn_shape(int64_t S, int d_e, int E, int F) {
-  const int rc = check_fp8_product(S, d_e, E, 8);
+  if (F <= 0) return MOE_ERR_INVALID_ARG;
+  if (F % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  const int rc = check_fp8_product(S, d_e, E, F);
   if (rc) return rc;
   return check_fp8_product(S, F, E, d_e);  // the down product contracts over F
 }

@@ -1545,11 +1545,6 @@ cudaError_t launch_few(const Operands& o, const Args& args, cudaStream_t s) {
 
 template <int MODE>
 int run_product(const Operands& o, const Args& args, cudaStream_t s) {
-  // units are counted in 31 bits (more would be a terabyte of weights or outputs),
-  // tiles too, even where segments behind a bad one overlap
-  if (max_tiles(args, kNt) > INT32_MAX / ((args.N + 127) / 128) ||
-      (args.S / kNt + 1) * args.E > INT32_MAX)
-    return MOE_ERR_UNSUPPORTED;
   const Choice c = choose(args, MODE == kGateUp);
   if (c.variant == 3) {
     const cudaError_t e = args.S == 1   ? launch_few<1>(o, args, s)
@@ -1587,6 +1582,13 @@ int run_product(const Operands& o, const Args& args, cudaStream_t s) {
 }
 
 }  // namespace
+
+// Units are counted in 31 bits (more would be a terabyte of weights or outputs),
+// tiles too, even where segments behind a bad one overlap.
+bool fp8_units_fit(int64_t S, int E, int N) {
+  return S / kNt + (S < E ? S : E) <= INT32_MAX / (((int64_t)N + 127) / 128) &&
+         (S / kNt + 1) * E <= INT32_MAX;
+}
 
 int grouped_fp8_run(const uint8_t* xq, const float* xs, const int32_t* offsets, int E, int64_t S,
                     int K, const uint8_t* w, const float* ws, int N, const __nv_bfloat16* residual,

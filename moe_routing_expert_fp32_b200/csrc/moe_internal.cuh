@@ -217,6 +217,8 @@ cudaError_t launch_quantize_blocks(const __nv_bfloat16* x, int64_t B, int64_t M,
 // offsets [E + 1], or nullptr with E = 1: one segment of all S rows.
 // early: offsets were complete before the kernel preceding on `s` started.
 // reset: the (first) kernel clears the status word, as reset_status would.
+// sizes it takes (checked before anything is enqueued): S rows, E segments, N columns
+bool fp8_units_fit(int64_t S, int E, int N);
 int grouped_fp8_run(const uint8_t* xq, const float* xs, const int32_t* offsets, int E, int64_t S,
                     int K, const uint8_t* w, const float* ws, int N, const __nv_bfloat16* residual,
                     __nv_bfloat16* y, DeviceStatus* st, cudaStream_t s, bool early, bool reset);
