@@ -474,10 +474,13 @@ MOE_API int moe_block_forward(const moe_bf16* x, int64_t N, const moe_block_dims
  * (S/32 + 1) * E below 2^31; e4m3 and bf16 pointers 16-byte aligned, scales
  * 4-byte aligned.
  * Scales are the caller's: any fp32 values, not only those that
- * moe_quantize_fp8 gives.  Products are summed in fp32: 128 columns of K in the
- * tensor core, times the product of the two scales (itself rounded to fp32),
- * then over the blocks in order; one rounding to bf16 at the end.  A call's
- * results depend on its arguments alone, bit for bit.  Outputs and workspace
+ * moe_quantize_fp8 gives.  Products are summed in fp32 with one rounding to bf16
+ * at the end: parts of a block of 128 columns (exact products, the whole block in
+ * the tensor core or 16 columns at a time), each times the product of its two
+ * scales (itself rounded to fp32), are added over the blocks.  The order of the
+ * additions goes by the sizes and the device's number of SMs, so the same row may
+ * round otherwise in a call of another number of rows; with equal arguments a
+ * call's results are equal, bit for bit.  Outputs and workspace
  * overlap neither each other nor an operand, but for moe_linear_fp8's y. */
 typedef uint8_t moe_fp8; /* e4m3 bit pattern (no infinities, NaN 0x7f) */
 
@@ -518,7 +521,8 @@ MOE_API int moe_linear_fp8(const moe_fp8* xq, const float* x_scale, int64_t M, i
  * offsets[E] <= S; w [E, N_out, K]; y [S, N_out] bf16.  Empty segments cost
  * nothing; rows from offsets[E] on are neither read nor written.  A segment
  * that runs backwards or past S is left out and recorded as
- * MOE_ERR_DEVICE_BOUNDS. */
+ * MOE_ERR_DEVICE_BOUNDS; rows that two of the others then share are written by
+ * both, in no order. */
 MOE_API size_t moe_grouped_linear_fp8_workspace_size(int64_t S, int K, int E, int N_out);
 MOE_API int moe_grouped_linear_fp8(const moe_fp8* xq, const float* x_scale,
                                    const int32_t* offsets, int E, int64_t S, int K,
@@ -538,7 +542,7 @@ typedef struct moe_fp8_experts {
 
 /* moe_expert_ffn on 8-bit operands: g = x . w1[e]^T and u = x . w3[e]^T in
  * fp32, h = act(g, u) in fp32 (moe_act_cfg's functions without their bf16
- * roundings), h to the 8-bit format per row and 128 columns as
+ * roundings, to about 2^-18; sigmoid is 0 below 2^-126), h to the 8-bit format per row and 128 columns as
  * moe_quantize_fp8 does (power-of-two scales with pow2_scales != 0),
  * y = bf16( h . w2[e]^T ).  offsets as in moe_grouped_linear_fp8; d_e and F
  * multiples of 16. */
