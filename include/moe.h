@@ -480,8 +480,8 @@ MOE_API int moe_block_forward(const moe_bf16* x, int64_t N, const moe_block_dims
  * scales (itself rounded to fp32), are added over the blocks.  The order of the
  * additions goes by the sizes and the device's number of SMs, so the same row may
  * round otherwise in a call of another number of rows; with equal arguments a
- * call's results are equal, bit for bit.  Outputs and workspace
- * overlap neither each other nor an operand, but for moe_linear_fp8's y. */
+ * call's results are equal, bit for bit.  Outputs and workspace overlap neither
+ * each other nor an operand, but for moe_linear_fp8's y. */
 typedef uint8_t moe_fp8; /* e4m3 bit pattern (no infinities, NaN 0x7f) */
 
 /* bf16 to the 8-bit format.  x [B, M, K] bf16; q [B, M, K] e4m3.
@@ -542,10 +542,10 @@ typedef struct moe_fp8_experts {
 
 /* moe_expert_ffn on 8-bit operands: g = x . w1[e]^T and u = x . w3[e]^T in
  * fp32, h = act(g, u) in fp32 (moe_act_cfg's functions without their bf16
- * roundings, to about 2^-18; sigmoid is 0 below 2^-126), h to the 8-bit format per row and 128 columns as
- * moe_quantize_fp8 does (power-of-two scales with pow2_scales != 0),
- * y = bf16( h . w2[e]^T ).  offsets as in moe_grouped_linear_fp8; d_e and F
- * multiples of 16. */
+ * roundings, to about 2^-18; sigmoid is 0 below 2^-126), h to the 8-bit format
+ * per row and 128 columns as moe_quantize_fp8 does (power-of-two scales with
+ * pow2_scales != 0), y = bf16( h . w2[e]^T ).  offsets as in
+ * moe_grouped_linear_fp8; d_e and F multiples of 16. */
 MOE_API size_t moe_expert_ffn_fp8_workspace_size(int64_t S, int d_e, int E, int F);
 MOE_API int moe_expert_ffn_fp8(const moe_fp8* xq, const float* x_scale, const int32_t* offsets,
                                int E, int64_t S, int d_e, int F, const moe_fp8_experts* w,

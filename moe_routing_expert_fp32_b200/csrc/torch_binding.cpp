@@ -149,8 +149,10 @@ PyObject* outputs(int rc, const T&... t) {
   } else {
     PyObject* items[] = {THPVariable_Wrap(t)...};
     PyObject* r = PyTuple_New(sizeof...(T));
+    for (PyObject* i : items)
+      if (!i) Py_CLEAR(r);  // an exception is set: no tuple with a hole in it
     for (size_t i = 0; i < sizeof...(T); ++i) {
-      if (r && items[i]) PyTuple_SET_ITEM(r, i, items[i]);
+      if (r) PyTuple_SET_ITEM(r, i, items[i]);
       else Py_XDECREF(items[i]);
     }
     return r;
