@@ -615,6 +615,11 @@ namespace {
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 int64_t ceil128(int64_t v) { return (v + 127) / 128; }
 
+// rows [rows, K] that k_quantize_rows takes (its grid: 32 blocks of 128 columns a CTA)
+bool quantize_rows_fit(int64_t rows, int K) {
+  return rows <= INT32_MAX * (int64_t)16 / ceil128(K);
+}
+
 int check_fp8_product(int64_t S, int K, int E, int N) {
   if (S < 0 || K <= 0 || E < 1 || N <= 0) return MOE_ERR_INVALID_ARG;
   if (E > 1024 || K % 16 != 0 || N % 8 != 0 || S > INT32_MAX) return MOE_ERR_UNSUPPORTED;
@@ -649,8 +654,9 @@ int moe_quantize_fp8(const moe_bf16* x, int64_t B, int64_t M, int K, int block_r
     return MOE_ERR_INVALID_ARG;
   if (K % 16 != 0 || K > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   if (B > INT32_MAX || M > INT32_MAX) return MOE_ERR_UNSUPPORTED;
-  const int64_t row_blocks = B * (block_rows == 1 ? M : ceil128(M));  // < 2^62
-  if (row_blocks > INT32_MAX * (int64_t)(block_rows == 1 ? 16 : 1) / ceil128(K))
+  // (products below 2^62)
+  if (block_rows == 1 ? !quantize_rows_fit(B * M, K)
+                      : B * ceil128(M) > INT32_MAX / ceil128(K))
     return MOE_ERR_UNSUPPORTED;
   const bool some = B > 0 && M > 0;
   if (some && (!x || !q || !scale)) return MOE_ERR_INVALID_ARG;
@@ -674,7 +680,7 @@ int moe_dispatch_fp8(const int32_t* topk_idx, int64_t N, int K, int E, const moe
   if (N < 0 || K < 1 || E < 1 || d_e <= 0) return MOE_ERR_INVALID_ARG;
   if (E > 1024 || K > 16) return MOE_ERR_UNSUPPORTED;
   if (d_e % 16 != 0 || d_e > (1 << 30)) return MOE_ERR_UNSUPPORTED;
-  if (N > INT32_MAX / K) return MOE_ERR_UNSUPPORTED;
+  if (N > INT32_MAX / K || !quantize_rows_fit(N, d_e)) return MOE_ERR_UNSUPPORTED;
   if (!counts || !offsets) return MOE_ERR_INVALID_ARG;
   if (N > 0 && (!topk_idx || !perm || !pos || !x_e || !xq || !x_scale)) return MOE_ERR_INVALID_ARG;
   if (N > 0 && (!aligned16(x_e) || !aligned16(xq) || !aligned4(x_scale))) return MOE_ERR_ALIGNMENT;
@@ -814,7 +820,8 @@ int check_forward_fp8(int64_t N, int d_r, int d_e, const moe_route_cfg* cfg, int
   if (rc) return rc;
   if (N < 0 || d_r <= 0) return MOE_ERR_INVALID_ARG;
   if (N > INT32_MAX / cfg->top_k || d_r % 32 != 0) return MOE_ERR_UNSUPPORTED;
-  return check_fp8_ffn_shape(N * cfg->top_k, d_e, cfg->num_experts, F);
+  if ((rc = check_fp8_ffn_shape(N * cfg->top_k, d_e, cfg->num_experts, F))) return rc;
+  return quantize_rows_fit(N, d_e) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 }  // namespace
 

@@ -61,16 +61,34 @@ def test_expert_mlp(m, p, S, E, d, F, no_device):
 
 @pytest.mark.parametrize("N,K,E,d,F", [(TILES // 16 - 1, 16, 1024, 32, 16),
                                        (TILES // 16, 16, 1024, 32, 16),
-                                       (7900, 1, 8, 2 ** 30, 16), (8192, 1, 8, 2 ** 30, 16)])
+                                       (4000, 1, 8, 2 ** 30, 16), (7900, 1, 8, 2 ** 30, 16),
+                                       (4000, 16, 16, 2 ** 30, 16)])
 def test_layer(m, p, N, K, E, d, F, no_device):
     """The layer refuses before its router and its sort run."""
     L = m.lib()
-    want = OK if fits(N * K, E, d) and fits(N * K, E, F) else -2
+    rows = N <= ROWS // -(-d // 128)
+    want = OK if fits(N * K, E, d) and fits(N * K, E, F) and rows else -2
     cfg = m.RouteConfig(E, 1, 1, K, 1.0)._c()
     assert (L.moe_forward_fp8_workspace_size(N, 32, d, ctypes.byref(cfg), F) > 0) == (want == OK)
     w, act = m._Fp8Experts(p, p, p, p, p, p), m.ActConfig("silu")._c()
     assert L.moe_forward_fp8(p, p, N, 32, d, p, None, ctypes.byref(cfg), ctypes.byref(w), F,
                              ctypes.byref(act), 0, p, None, None, p, HUGE, None) == want
+
+
+ROWS = (2 ** 31 - 1) * 16  # blocks of 128 columns of the rows that are quantised
+
+
+@pytest.mark.parametrize("N,K,d,want", [
+    (2 ** 27, 8, 2 ** 30, -2), (2 ** 27, 8, 128, OK), (ROWS // 2 ** 23, 8, 2 ** 30, OK),
+    (ROWS // 2 ** 23 + 1, 8, 2 ** 30, -2), (2 ** 31 - 1, 1, 2048, OK), (2 ** 31 - 1, 1, 2064, -2)])
+def test_rows_of_the_dispatch(m, p, N, K, d, want, no_device):
+    """A grid that would not cover the rows is refused, as the quantisation's is."""
+    L = m.lib()
+    assert L.moe_dispatch_fp8(p, N, K, 16, p, d, 0, p, p, p, p, p, p, p, HUGE, None) == want
+    assert L.moe_quantize_fp8(p, 1, N, d, 1, 0, p, p, None) == want
+    cfg = m.RouteConfig(1024, 1, 1, K, 1.0)._c()
+    if want != OK:
+        assert L.moe_forward_fp8_workspace_size(N, 32, d, ctypes.byref(cfg), 16) == 0
 
 
 @pytest.fixture
