@@ -1275,8 +1275,11 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
     // weights from HBM, the mean time with 4, 5, 6, 7 and 8 was 0.95, 0.95, 0.96, 1 and
     // 1.00 at one row, 0.95, 0.96, 0.98, 1 and 1.03 at two, 0.98, 0.99, 1.00, 1 and 1.03
     // at four (1 row, N = 2048: K = 2048 2.9, 2.9, 3.0, 3.1, 3.1 us, K = 4096 4.2, 4.5,
-    // 4.7, 5.0, 4.4, K = 7168 6.3, 6.0, 6.4, 6.2, 6.3).
-    constexpr int kBatch = 4;
+    // 4.7, 5.0, 4.4, K = 7168 6.3, 6.0, 6.4, 6.2, 6.3).  With 4, one row needs 64
+    // registers and two CTAs fit on an SM: a launch whose CTAs are placed while the one
+    // before it still holds its SMs then doubles up on the others, and calls in a loop took
+    // 5.2 or 7.9 us from one run to the next (K = 7168, N = 2048; 5.1 with 5).
+    constexpr int kBatch = 5;
     for (int k0 = 16 * lane; k0 - 16 * lane < a.K; k0 += 512 * kBatch) {
       uint4 v[kBatch];
       float f[kBatch][M];
@@ -1473,7 +1476,7 @@ size_t few_smem(int64_t M, int K) { return (size_t)M * ((K + 511) / 512) * 512 *
 // decode against 256 rows 78 and 92 with 8 rows each, 86 and 96 with 32, 147
 // and 95 with 40; 16 segments, K = N = 512, 128 rows each: decode, 128 and 256
 // rows 7.6, 6.3 and 8.4.  Few rows against decode, K = 7168: one row 5.1 and 8.5
-// with N = 2048, 37 and 24 with N = 18944; two rows 7.2 and 8.5, three 9.5 and 8.5
+// with N = 2048, 33 and 24 with N = 18944; two rows 7.2 and 8.5, three 9.5 and 8.5
 // with N = 2048.  One segment, K = 7168, N = 2048: decode split 4 ways, not
 // split, 128 and 256 rows 9.5, 21, 23 and 36 with 16 rows; decode, 128 and 256 rows
 // 41, 26 and 39 with 384; 135, 51 and 40 with 2048.  K = N = 512, 64 rows: split
