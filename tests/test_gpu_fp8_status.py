@@ -46,7 +46,7 @@ def test_no_memory_of_another_stream_is_cleared(call):
 a, b = torch.cuda.Stream(), torch.cuda.Stream()
 with torch.cuda.stream(a):
     small = [torch.full((64,), 7, dtype=torch.int32, device="cuda") for _ in range(8)]
-    torch.cuda._sleep(400_000_000)
+    torch.cuda._sleep(1_500_000_000)
     read = [t.clone() for t in small]
     del small
     call(y)
